@@ -294,6 +294,29 @@ TP_API tp_status tp_vocab_cross_entropy(tp_plan* plan, int64_t T, const void* co
                                         const int32_t* labels, float grad_scale, float* loss,
                                         float* lse, void* const* dlogits, void* stream);
 
+/* Output head and cross-entropy in one call, without the logits: what
+ * tp_column_fwd with TP_VOCAB, tp_vocab_cross_entropy and
+ * tp_column_bwd_reduce compute together ([TP-blog] §6.2), with the scores
+ * z = X W^T kept in fp32 until the loss and never stored for all tokens.
+ *   X [T, hidden]; W[i] [Vp/p, hidden] shard i of the head weight; labels [T]
+ *   int32 (device; < 0 = ignored token, >= vocab sets the device status and is
+ *   ignored). loss [T] fp32 = logsumexp over the real vocab columns minus the
+ *   target score (0 for ignored tokens); lse [T] fp32 (NULL ok).
+ *   dX [T, hidden] (NULL skips) = sum_i d_i W[i] and dW[i] [Vp/p, hidden] (NULL
+ *   array skips) = d_i^T X, with d = (softmax - onehot) * grad_scale, rounded to
+ *   the plan dtype before the two products; sums are fp32 and rounded once.
+ *   Padding rows of dW are zero. dX and dW must not alias X and W.
+ *   chunk: tokens whose scores are worked on at a time (0: the library's choice);
+ *   the workspace holds them as 2 (bf16) or 4 (fp32) bytes per token and padded
+ *   vocab entry, plus, when T > chunk and dW is wanted, fp32 sums of dW. Without
+ *   gradients only per-row statistics of the score tiles are kept.
+ * With T = 0, dW is set to zero. The workspace belongs to the plan and grows on
+ * demand: make a call of the same sizes before capturing one. */
+TP_API tp_status tp_vocab_linear_cross_entropy(tp_plan* plan, int64_t T, const void* X, const void* const* W,
+                                               const int32_t* labels, float grad_scale, float* loss,
+                                               float* lse, void* dX, void* const* dW, int64_t chunk,
+                                               void* stream);
+
 /* LayerNorm / RMSNorm of rows whose hidden dim is split over the p shards,
  * with the statistics formed the way [TP-blog] §3.3 describes: every shard's
  * local sums (sum x and sum x^2; RMSNorm only sum x^2) are summed over shards

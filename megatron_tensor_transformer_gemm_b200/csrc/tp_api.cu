@@ -224,6 +224,42 @@ tp_status workspace2(tp_plan* plan, size_t bytes, void** out) {
   return TP_OK;
 }
 
+tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out) {
+  int dev = 0;
+  TP_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  TP_TRY(cuda_status(cudaStreamIsCapturing(st, &cs), "cudaStreamIsCapturing"));
+  const bool capturing = cs != cudaStreamCaptureStatusNone;
+  if (!plan->sc || plan->sc_bytes < bytes || plan->sc_device != dev) {
+    if (capturing)
+      return fail(TP_ERR_ARG, "the plan's workspace must grow to %zu bytes: make the call once before the stream capture",
+                  bytes);
+    if (plan->sc && plan->sc_captured) {
+      Retired* r = new (std::nothrow) Retired{plan->sc, plan->sc_device, plan->sc_retired};
+      if (!r) return fail(TP_ERR_ARG, "out of host memory for the plan's workspace");
+      plan->sc_retired = r;
+    } else if (plan->sc) {
+      // an earlier call may still use the block, on any stream of its device
+      if (plan->sc_device != dev) cudaSetDevice(plan->sc_device);
+      cudaDeviceSynchronize();
+      cudaFree(plan->sc);
+      if (plan->sc_device != dev) cudaSetDevice(dev);
+    }
+    plan->sc = nullptr;
+    plan->sc_bytes = 0;
+    plan->sc_captured = 0;
+    const size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
+    void* p = nullptr;
+    TP_TRY(cuda_status(cudaMalloc(&p, want), "cudaMalloc(scratch)"));
+    plan->sc = p;
+    plan->sc_bytes = want;
+    plan->sc_device = dev;
+  }
+  if (capturing) plan->sc_captured = 1;
+  *out = plan->sc;
+  return TP_OK;
+}
+
 tp_status check_ptr(const void* p, const char* name) {
   if (!p) return fail(TP_ERR_ARG, "%s is NULL", name);
   if (!aligned16(p)) return fail(TP_ERR_ALIGN, "%s (%p) is not 16-byte aligned", name, p);
@@ -436,24 +472,9 @@ tp_status run_wgrad(tp_plan* plan, GemmBatch w, cudaStream_t st, bool allow_spli
   if (plan->dtype != TP_BF16) return run_gemm(plan, w, st);
   const int s = wgrad_split(plan, w, allow_split);
   if (s <= 1) return launch_gemm_bf16(w, st);
-  const int n = w.n;
-  const int64_t M = w.g[0].M, N = w.g[0].N, mn = M * N, elems = n * mn;
   void* ws = nullptr;
-  TP_TRY(workspace(plan, static_cast<size_t>(s) * elems * sizeof(float), &ws));
-  float* part = static_cast<float*>(ws);
-  MutPtrArray outs{};
-  for (int i = 0; i < n; ++i) {
-    outs.p[i] = w.g[i].D;
-    w.g[i].D = part + i * mn;
-  }
-  w.ksplit = s;
-  w.split_stride = elems;
-  w.out_f32 = true;
-  TP_TRY(launch_gemm_bf16(w, st));
-  PtrArray P{};
-  for (int j = 0; j < s; ++j) P.p[j] = part + j * elems;
-  return launch_reduce(P, s, nullptr, nullptr, PtrArray{}, false, outs, true, n, n * M, N, TP_F32,
-                       TP_BF16, st);
+  TP_TRY(workspace(plan, static_cast<size_t>(s) * w.n * w.g[0].M * w.g[0].N * sizeof(float), &ws));
+  return launch_gemm_split(w, s, static_cast<float*>(ws), st);
 }
 
 // Launch the weight gradients a row backward left waiting, alone, on the
@@ -601,6 +622,19 @@ void tp_plan_destroy(tp_plan* plan) {
     cudaSetDevice(plan->ws2_device);
     cudaDeviceSynchronize();
     cudaFree(plan->ws2);
+  }
+  if (plan->sc) {
+    cudaSetDevice(plan->sc_device);
+    cudaDeviceSynchronize();
+    cudaFree(plan->sc);
+  }
+  while (plan->sc_retired) {
+    tpi::Retired* r = plan->sc_retired;
+    plan->sc_retired = r->next;
+    cudaSetDevice(r->device);
+    cudaDeviceSynchronize();
+    cudaFree(r->p);
+    delete r;
   }
   cudaSetDevice(cur);
   cudaGetLastError();
@@ -1249,6 +1283,40 @@ tp_status tp_vocab_cross_entropy(tp_plan* plan, int64_t T, const void* const* lo
     for (int i = 0; i < p; ++i) g.p[i] = dlogits[i];
   return launch_vocab_ce(to_arr(logits, p), g, p, plan->vocab_padded / p, plan->vocab, labels,
                          grad_scale, loss, lse, T, plan->dtype, as_stream(stream));
+}
+
+tp_status tp_vocab_linear_cross_entropy(tp_plan* plan, int64_t T, const void* X, const void* const* W,
+                                        const int32_t* labels, float grad_scale, float* loss, float* lse,
+                                        void* dX, void* const* dW, int64_t chunk, void* stream) {
+  TP_TRY(check_plan(plan));
+  TP_TRY(check_T(T));
+  if (plan->vocab_padded <= 0) return fail(TP_ERR_ARG, "plan has no vocab (tp_plan_set_vocab)");
+  if (chunk < 0) return fail(TP_ERR_ARG, "chunk = %lld is negative", static_cast<long long>(chunk));
+  const int p = plan->p, h = plan->hidden;
+  TP_TRY(check_ptrs(W, p, "W", false));
+  if (T > 0) {  // an empty tensor has no address
+    TP_TRY(check_ptr(X, "X"));
+    TP_TRY(check_ptr(labels, "labels"));
+    TP_TRY(check_ptr(loss, "loss"));
+    if (lse) TP_TRY(check_ptr(lse, "lse"));
+    if (dX) TP_TRY(check_ptr(dX, "dX"));
+  }
+  TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dW), p, "dW", true));
+  TP_TRY(check_row_bytes(h, plan->dtype, "hidden"));
+  // gradients overwrite nothing that a later step of the call reads
+  if (T > 0 && dX == X) return fail(TP_ERR_ARG, "dX must not alias X");
+  for (int i = 0; dW && i < p; ++i)
+    for (int j = 0; j < p; ++j)
+      if (dW[i] == W[j]) return fail(TP_ERR_ARG, "dW[%d] must not alias W[%d]", i, j);
+  cudaStream_t st = as_stream(stream);
+  if (dW) TP_TRY(flush_wgrad(plan));
+  if (T == 0) {  // no token: the weight gradient is zero
+    const size_t bytes = static_cast<size_t>(plan->vocab_padded / p) * h * dsize(plan->dtype);
+    for (int i = 0; dW && i < p; ++i)
+      TP_TRY(cuda_status(cudaMemsetAsync(dW[i], 0, bytes, st), "cudaMemsetAsync(dW)"));
+    return TP_OK;
+  }
+  return launch_vocab_linear_ce(plan, T, X, to_arr(W, p), labels, grad_scale, loss, lse, dX, to_marr(dW, p), chunk, st);
 }
 
 static tp_status check_norm_sharded(const tp_plan* plan, tp_norm_kind kind, int64_t rows) {

@@ -87,6 +87,8 @@ struct GroupArgs {
   const void* bias;
   const void* aux;
   int64_t ldaux;
+  const float* acc;
+  int64_t ldacc;
 };
 
 struct alignas(64) GemmParams {
@@ -279,6 +281,16 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
           load_row_chunk_bf16(res, ga.ldaux, orow, j0, ga.N, r);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] += r[i];
+        }
+        if (ga.acc) {  // this thread's own 32 columns, read before it stores them
+          const float* a = ga.acc + static_cast<int64_t>(row) * ga.ldacc + j0;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (j0 + q * 4 < ga.N) {
+              const float4 f = *reinterpret_cast<const float4*>(a + q * 4);
+              v[q * 4 + 0] += f.x; v[q * 4 + 1] += f.y; v[q * 4 + 2] += f.z; v[q * 4 + 3] += f.w;
+            }
+          }
         }
         if (p.out_f32) store_row_chunk_f32(dst, ga.ldd, orow, j0, ga.N, v);
         else store_row_chunk_bf16(dst, ga.ldd, orow, j0, ga.N, v);
@@ -1092,6 +1104,7 @@ bool tma_epilogue_ok(const GemmBatch& b, int nout, int ksplit) {
   const bool halves = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_DSWIGLU;
   for (int i = 0; i < nout; ++i) {
     const GemmProblem& o = b.g[i];
+    if (o.acc) return false;
     const void* out = fwd ? o.D2 : o.D;  // the output every tile writes
     if (!out || reinterpret_cast<uintptr_t>(out) % 16) return false;
     if (fwd && o.D && reinterpret_cast<uintptr_t>(o.D) % 16) return false;
@@ -1305,6 +1318,9 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
     return fail(TP_ERR_ARG, "K-concatenated GEMM supports the plain epilogue only");
   const int nout = b.kcat ? 1 : b.n;
   for (int i = 0; i < nout; ++i)
+    if (b.g[i].acc && (b.epi != EPI_STORE || b.ksplit > 1 || b.scatter_n || b.g[i].ldacc % 4 || !aligned16(b.g[i].acc)))
+      return fail(TP_ERR_ARG, "GEMM %d: a running sum needs a plain dense output and 16-byte rows", i);
+  for (int i = 0; i < nout; ++i)
     if (b.g[i].M <= 0 || b.g[i].N <= 0)
       return fail(TP_ERR_ARG, "GEMM %d has an empty output (%d x %d)", i, b.g[i].M, b.g[i].N);
   const int sms = device_sms();
@@ -1349,6 +1365,8 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
       a.bias = o.bias;
       a.aux = o.aux;
       a.ldaux = o.ldaux;
+      a.acc = o.acc;
+      a.ldacc = o.ldacc;
       const int64_t t = static_cast<int64_t>((o.M + tile_m - 1) / tile_m) * a.tiles_n;
       if (tiles + t > 0x7fffffffLL) return fail(TP_ERR_UNSUPPORTED, "too many GEMM tiles");
       tiles += static_cast<int>(t);
@@ -1487,6 +1505,81 @@ int gemm_split_k(const GemmBatch& b) {
   }
   const int kbps = (nkb + best - 1) / best;
   return (nkb + kbps - 1) / kbps;  // every split gets at least one K block
+}
+
+tp_status launch_gemm_split(GemmBatch w, int s, float* part, cudaStream_t st) {
+  const int n = w.n;
+  const int64_t M = w.g[0].M, N = w.g[0].N, mn = M * N, elems = n * mn;
+  MutPtrArray outs{};
+  for (int i = 0; i < n; ++i) {
+    outs.p[i] = w.g[i].D;
+    w.g[i].D = part + i * mn;
+  }
+  w.ksplit = s;
+  w.split_stride = elems;
+  w.out_f32 = true;
+  tp_status r = launch_gemm_bf16(w, st);
+  if (r != TP_OK) return r;
+  PtrArray P{};
+  for (int j = 0; j < s; ++j) P.p[j] = part + j * elems;
+  return launch_reduce(P, s, nullptr, nullptr, PtrArray{}, false, outs, true, n, n * M, N, TP_F32,
+                       TP_BF16, st);
+}
+
+int gemm_cat_split(const GemmBatch& b) {
+  if (!b.kcat || b.scatter_n || b.epi != EPI_STORE || b.n < 1) return 0;
+  for (int i = 0; i < b.n; ++i)
+    if (b.g[i].K != b.g[0].K || b.g[i].bias || b.g[i].aux || b.g[i].acc) return 0;
+  const int sms = device_sms();
+  const int nkb = (b.g[0].K + BK - 1) / BK;
+  double best_cost = 0.0;
+  choose_layout(b, sms, &best_cost);
+  int best = 0;
+  GemmBatch t = b;
+  t.kcat = false;
+  t.out_f32 = true;
+  for (int i = 1; i < b.n; ++i) {
+    t.g[i].M = b.g[0].M;
+    t.g[i].N = b.g[0].N;
+  }
+  const double out = static_cast<double>(b.g[0].M) * b.g[0].N;
+  for (int s = 1; s * b.n <= TP_MAX_SHARDS; ++s) {
+    if (s * b.n == 1) continue;
+    if (s > 1 && nkb < 4 * s) break;
+    const int kbps = (nkb + s - 1) / s;
+    if ((nkb + kbps - 1) / kbps != s) continue;  // a split would be empty
+    t.ksplit = s;
+    double c = 0.0;
+    choose_layout(t, sms, &c);
+    c += out * (4.0 * s * b.n + 2.0) / 6000.0 + 1600.0;  // the partials' reduce, as in gemm_split_k
+    if (c < 0.9 * best_cost) {
+      best_cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+tp_status launch_gemm_cat_split(GemmBatch b, int s, float* part, cudaStream_t st) {
+  const int n = b.n;
+  const int64_t M = b.g[0].M, N = b.g[0].N, mn = M * N;
+  MutPtrArray out{};
+  out.p[0] = b.g[0].D;
+  for (int i = 0; i < n; ++i) {
+    b.g[i].M = static_cast<int>(M);
+    b.g[i].N = static_cast<int>(N);
+    b.g[i].D = part + i * mn;
+    b.g[i].ldd = N;
+  }
+  b.kcat = false;
+  b.out_f32 = true;
+  b.ksplit = s;
+  b.split_stride = n * mn;
+  tp_status r = launch_gemm_bf16(b, st);
+  if (r != TP_OK) return r;
+  PtrArray P{};
+  for (int j = 0; j < s * n; ++j) P.p[j] = part + j * mn;
+  return launch_reduce(P, s * n, nullptr, nullptr, PtrArray{}, false, out, false, 1, M, N, TP_F32, TP_BF16, st);
 }
 
 }  // namespace tpi

@@ -10,6 +10,12 @@
 
 namespace tpi {
 struct GemmBatch;
+// A scratch block kept for the captured graphs that use it.
+struct Retired {
+  void* p;
+  int device;
+  Retired* next;
+};
 }
 
 struct tp_plan {
@@ -44,6 +50,13 @@ struct tp_plan {
   int group_wgrad;
   tpi::GemmBatch* wg_pend;  // NULL when nothing waits
   cudaStream_t wg_st;
+  // Scratch of the calls that may be captured into graphs (tpi::scratch):
+  // a block that a captured graph may hold is never freed before the plan.
+  void* sc;
+  size_t sc_bytes;
+  int sc_device;
+  int sc_captured;
+  tpi::Retired* sc_retired;
 };
 
 namespace tpi {
@@ -102,6 +115,13 @@ tp_status plan_counters(tp_plan* plan, cudaStream_t st, unsigned** out);
 // Scratch for the work a deferred backward puts on the side stream (never
 // shared with the caller's stream).
 tp_status workspace2(tp_plan* plan, size_t bytes, void** out);
+
+// Scratch of at least `bytes` on the current device for a call on `st`, owned
+// by the plan and shared by its calls in turn. Growing it allocates, so inside
+// a stream capture a call that needs more than the plan holds is refused
+// (TP_ERR_ARG); a block handed out inside a capture stays allocated until the
+// plan is destroyed, since the graph replays with its address.
+tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out);
 
 // Validation helpers: each returns TP_OK or records an error.
 tp_status check_ptr(const void* p, const char* name);
@@ -163,6 +183,11 @@ tp_status launch_vocab_ce(const PtrArray& L, const MutPtrArray& G, int p, int64_
                           const int32_t* labels, float scale, float* loss, float* lse, int64_t T,
                           tp_dtype dt, cudaStream_t st);
 
+// Output head and cross-entropy without the logits (tp_loss.cu).
+tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const PtrArray& W,
+                                 const int32_t* labels, float scale, float* loss, float* lse, void* dX,
+                                 const MutPtrArray& dW, int64_t chunk, cudaStream_t st);
+
 // Norms of hidden-sharded rows (tp_layernorm.cu).
 tp_status launch_norm_sharded_fwd(bool rms, const PtrArray& X, const PtrArray& G,
                                   const PtrArray& B, const MutPtrArray& Y, int p, int64_t rows,
@@ -201,6 +226,10 @@ struct GemmProblem {
   const void* aux;   // Z for EPI_DGELU / EPI_DSWIGLU
   int64_t ldaux;
   int nh;            // SwiGLU: columns of each half ([Zg|Zu] offset of Zu)
+  // fp32 running sum [M, N] (row stride ldacc) added to the product, EPI_STORE
+  // only; may be D itself when D is fp32.
+  const float* acc;
+  int64_t ldacc;
 };
 
 struct GemmBatch {
@@ -239,6 +268,16 @@ bool gemm_fills_gpu(const GemmBatch& b);
 // The K split that minimises the estimated time of a batch of plain bf16-output
 // GEMMs of equal shape, counting the fp32 partials' reduce (1 = no split, <= 16).
 int gemm_split_k(const GemmBatch& b);
+// b (plain bf16 outputs D[i], dense [M, N], one shape) with its K split s ways:
+// the splits' fp32 partials go to `part` (s * n * M * N floats) and one reduce
+// adds them in order into D[i].
+tp_status launch_gemm_split(GemmBatch b, int s, float* part, cudaStream_t st);
+// The K-concatenated batch b (one bf16 output, D dense [M, N], equal segments) as
+// n * s separate partial products (n * s <= 16) and one ordered reduce, or as
+// it is: the s that takes least time by the estimate, 0 for the latter. Few
+// output tiles with a long K gain from it.
+int gemm_cat_split(const GemmBatch& b);
+tp_status launch_gemm_cat_split(GemmBatch b, int s, float* part, cudaStream_t st);
 // fp32 FMA path (tp_gemm_simt.cu): the same epilogues, grouping and K concatenation.
 tp_status launch_gemm_f32(const GemmBatch& b, cudaStream_t st);
 

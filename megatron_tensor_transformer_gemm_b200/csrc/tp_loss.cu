@@ -1,0 +1,250 @@
+// Output head fused with its softmax cross-entropy (TP walkthrough 2kiu.com
+// §6.2): loss, log-sum-exp and the gradients of X and of the vocab-sharded
+// head weight from X and W, without keeping the scores z = X W^T.
+//
+//   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label
+//   d_tv  = (exp(z_tv - lse_t) - [v = label]) * scale,  dX = d W,  dW = d^T X
+//
+// Tokens are taken a chunk at a time; the workspace holds one chunk's scores.
+#include <algorithm>
+
+#include "tp_device.cuh"
+#include "tp_internal.h"
+
+namespace {
+
+using tpi::GemmBatch;
+using tpi::GemmProblem;
+using tpi::MutPtrArray;
+using tpi::PtrArray;
+
+constexpr unsigned kStatusBadIndex = 2u;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// (max, sum of 2^(x - max)) pairs in the log2 domain; {-inf, 0} is the empty set.
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, a.y + b.y);  // nothing yet (or NaN sums)
+  return make_float2(m, a.y * tpd::ex2(a.x - m) + b.y * tpd::ex2(b.x - m));
+}
+
+template <int THREADS>
+__device__ __forceinline__ float2 block_merge(float2 v, float2* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  float2 t = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) t = merge(t, red[w]);
+  return t;
+}
+
+// One CTA per token row of fp32 scores z [rows, ld]: a pass for the running
+// (max, sum), then (d != NULL) a pass that writes d, which may be z itself.
+constexpr int kRowThreads = 512;
+template <typename Out>
+__global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, int64_t ld, int vocab, const int32_t* labels,
+                                                              float scale, float* loss, float* lse_out, Out* d,
+                                                              unsigned* status) {
+  tpd::pdl_entry();
+  __shared__ float2 red[kRowThreads / 32];
+  const int64_t t = blockIdx.x;
+  const int label = labels[t];
+  const bool ignore = label < 0 || label >= vocab;
+  const float* row = z + t * ld;
+  float2 acc = make_float2(-INFINITY, 0.f);
+  for (int c = threadIdx.x * 4; c < vocab; c += kRowThreads * 4) {
+    const float4 u = *reinterpret_cast<const float4*>(row + c);
+    float x[4] = {u.x, u.y, u.z, u.w};
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = c + e < vocab ? x[e] * kLog2e : -INFINITY;
+      m = fmaxf(m, x[e]);
+    }
+    const float mo = m == -INFINITY ? 0.f : m;
+    acc = merge(acc, make_float2(m, tpd::ex2(x[0] - mo) + tpd::ex2(x[1] - mo) + tpd::ex2(x[2] - mo) + tpd::ex2(x[3] - mo)));
+  }
+  const float2 tot = block_merge<kRowThreads>(acc, red);
+  const float lse2 = tot.x + log2f(tot.y);
+  if (threadIdx.x == 0) {
+    if (label >= vocab) atomicOr(status, kStatusBadIndex);
+    loss[t] = ignore ? 0.f : lse2 * kLn2 - row[label];
+    if (lse_out) lse_out[t] = lse2 * kLn2;
+  }
+  if (!d) return;
+  __syncthreads();  // the label's score has been read: d may be z
+  Out* drow = d + t * ld;
+  for (int64_t c = threadIdx.x * 4; c < ld; c += kRowThreads * 4) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!ignore && c < vocab) {
+      const float4 u = *reinterpret_cast<const float4*>(row + c);
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float pr = c + e < vocab ? tpd::ex2(fmaf(x[e], kLog2e, -lse2)) : 0.f;
+        x[e] = (pr - (c + e == label ? 1.f : 0.f)) * scale;
+      }
+    }
+    if constexpr (sizeof(Out) == 2)
+      *reinterpret_cast<uint2*>(drow + c) = make_uint2(tpd::pack_bf16x2(x[0], x[1]), tpd::pack_bf16x2(x[2], x[3]));
+    else
+      *reinterpret_cast<float4*>(drow + c) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Tokens per chunk: the caller's, or one chunk for all tokens unless chunks of
+// about 1 GiB of scores make the workspace (scores and fp32 sums of dW) smaller.
+int64_t pick_chunk(int64_t T, int64_t Vp, int64_t h, size_t score_bytes, bool dw_sums, int64_t asked) {
+  if (asked > 0) return std::min(asked, T);
+  const double all = static_cast<double>(T) * Vp * score_bytes;
+  const double part = static_cast<double>(1u << 30);
+  if (all <= part + (dw_sums ? 4.0 * Vp * h : 0.0)) return T;
+  const int64_t most = std::max<int64_t>(1024, static_cast<int64_t>(part / (static_cast<double>(Vp) * score_bytes)) / 256 * 256);
+  const int64_t n = (T + most - 1) / most;
+  return std::min(T, ((T + n - 1) / n + 255) / 256 * 256);
+}
+
+}  // namespace
+
+namespace tpi {
+
+tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const PtrArray& W, const int32_t* labels,
+                                 float scale, float* loss, float* lse, void* dX, const MutPtrArray& dW, int64_t chunk,
+                                 cudaStream_t st) {
+  const bool bf = plan->dtype == TP_BF16;
+  const int p = plan->p, h = plan->hidden, V = plan->vocab, Vp = plan->vocab_padded, Vs = Vp / p;
+  const size_t es = dsize(plan->dtype);
+  const bool grad = dX || dW.p[0], dw = dW.p[0] != nullptr;
+  const int64_t Tc = pick_chunk(T, Vp, h, bf ? 6 : 4, bf && dw, chunk);
+  const int64_t nch = (T + Tc - 1) / Tc;
+  unsigned* status = nullptr;
+  TP_TRY(device_status_word(&status));
+
+  // products with d of a chunk of n tokens starting at token t0
+  auto dx_batch = [&](const void* d, int64_t t0, int64_t n) {
+    GemmBatch b{};
+    b.n = p;
+    b.b_mn = true;
+    b.epi = EPI_STORE;
+    b.out_f32 = !bf;
+    b.kcat = true;
+    for (int i = 0; i < p; ++i) {
+      GemmProblem& g = b.g[i];
+      g.M = static_cast<int>(n);
+      g.N = h;
+      g.K = Vs;
+      g.A = static_cast<const uint8_t*>(d) + static_cast<size_t>(i) * Vs * es;
+      g.lda = Vp;
+      g.B = W.p[i];
+      g.ldb = h;
+      g.D = static_cast<uint8_t*>(dX) + static_cast<size_t>(t0) * h * es;
+      g.ldd = h;
+    }
+    return b;
+  };
+  auto dw_batch = [&](const void* d, int64_t t0, int64_t n) {
+    GemmBatch b{};
+    b.n = p;
+    b.a_mn = b.b_mn = true;
+    b.epi = EPI_STORE;
+    b.out_f32 = !bf;
+    for (int i = 0; i < p; ++i) {
+      GemmProblem& g = b.g[i];
+      g.M = Vs;
+      g.N = h;
+      g.K = static_cast<int>(n);
+      g.A = static_cast<const uint8_t*>(d) + static_cast<size_t>(i) * Vs * es;
+      g.lda = Vp;
+      g.B = static_cast<const uint8_t*>(X) + static_cast<size_t>(t0) * h * es;
+      g.ldb = h;
+      g.D = dW.p[i];
+      g.ldd = h;
+    }
+    return b;
+  };
+
+  // scratch: fp32 scores | d | fp32 sums of dW | split-K partials
+  const int sx = bf && dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 0;
+  const int sw = bf && dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
+  const size_t z_bytes = round256(static_cast<size_t>(Tc) * Vp * 4);
+  const size_t d_bytes = bf && grad ? round256(static_cast<size_t>(Tc) * Vp * 2) : 0;
+  const size_t acc_bytes = bf && dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
+  const size_t part_bytes = std::max(static_cast<size_t>(sx) * p * Tc * h * 4, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
+  void* ws = nullptr;
+  TP_TRY(scratch(plan, z_bytes + d_bytes + acc_bytes + part_bytes, st, &ws));
+  float* z = static_cast<float*>(ws);
+  uint8_t* db = static_cast<uint8_t*>(ws) + (bf ? z_bytes : 0);
+  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + z_bytes + d_bytes);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + z_bytes + d_bytes + acc_bytes);
+
+  for (int64_t c = 0; c < nch; ++c) {
+    const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
+    GemmBatch b{};
+    b.n = p;
+    b.epi = EPI_STORE;
+    b.out_f32 = true;
+    for (int i = 0; i < p; ++i) {
+      GemmProblem& g = b.g[i];
+      g.M = static_cast<int>(n);
+      g.N = Vs;
+      g.K = h;
+      g.A = static_cast<const uint8_t*>(X) + static_cast<size_t>(t0) * h * es;
+      g.lda = h;
+      g.B = W.p[i];
+      g.ldb = h;
+      g.D = z + static_cast<size_t>(i) * Vs;
+      g.ldd = Vp;
+    }
+    TP_TRY(bf ? launch_gemm_bf16(b, st) : launch_gemm_f32(b, st));
+    if (bf)
+      (void)launch(ce_rows_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st, z,
+                   static_cast<int64_t>(Vp), V, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
+                   grad ? reinterpret_cast<__nv_bfloat16*>(db) : nullptr, status);
+    else
+      (void)launch(ce_rows_kernel<float>, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st, z,
+                   static_cast<int64_t>(Vp), V, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
+                   grad ? reinterpret_cast<float*>(db) : nullptr, status);
+    TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
+    if (dX) {
+      const GemmBatch x = dx_batch(db, t0, n);
+      const int s = bf ? (n == Tc ? sx : 0) : 0;
+      if (!bf) TP_TRY(launch_gemm_f32(x, st));
+      else if (s > 0) TP_TRY(launch_gemm_cat_split(x, s, part, st));
+      else TP_TRY(launch_gemm_bf16(x, st));
+    }
+    if (dw) {
+      GemmBatch w = dw_batch(db, t0, n);
+      if (!bf) {  // the fp32 output is its own running sum
+        if (c > 0)
+          for (int i = 0; i < p; ++i) {
+            w.g[i].aux = w.g[i].D;
+            w.g[i].ldaux = h;
+          }
+        TP_TRY(launch_gemm_f32(w, st));
+      } else if (sw > 1) {
+        TP_TRY(launch_gemm_split(w, sw, part, st));
+      } else {
+        for (int i = 0; nch > 1 && i < p; ++i) {
+          float* a = acc + static_cast<size_t>(i) * Vs * h;
+          if (c > 0) {
+            w.g[i].acc = a;
+            w.g[i].ldacc = h;
+          }
+          if (c < nch - 1) w.g[i].D = a;
+        }
+        w.out_f32 = c < nch - 1;
+        TP_TRY(launch_gemm_bf16(w, st));
+      }
+    }
+  }
+  return TP_OK;
+}
+
+}  // namespace tpi

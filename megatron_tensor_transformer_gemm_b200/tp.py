@@ -97,6 +97,8 @@ _SIGS = {
     "tp_embedding_fwd": (_int, [_plan_p, _i64, _vp, _vpp, _vp, _vp]),
     "tp_embedding_bwd": (_int, [_plan_p, _i64, _vp, _vp, _vpp, _vp]),
     "tp_vocab_cross_entropy": (_int, [_plan_p, _i64, _vpp, _vp, ctypes.c_float, _fp, _fp, _vpp, _vp]),
+    "tp_vocab_linear_cross_entropy": (_int, [_plan_p, _i64, _vp, _vpp, _vp, ctypes.c_float, _fp, _fp, _vp, _vpp,
+                                             _i64, _vp]),
     "tp_norm_sharded_fwd": (_int, [_plan_p, _int, _i64, _vpp, _vpp, _vpp, _vpp, _fp, _fp, _vp]),
     "tp_norm_sharded_bwd": (_int, [_plan_p, _int, _i64, _vpp, _vpp, _vpp, _fp, _fp, _vpp, _vpp, _vpp, _vp]),
     "tp_row_fwd_reduce": (_int, [_plan_p, _int, _i64, _vpp, _vpp, _vp, _vp, _vp, _vp]),
@@ -228,6 +230,48 @@ def _stream(stream=None) -> int | None:
 DTYPES = {"bf16": TP_BF16, "f32": TP_F32}
 
 
+def _want(name: str, t, shape: tuple, *dtypes) -> None:
+    """ValueError unless t is a dense tensor of that shape and one of the dtypes (None is not checked)."""
+    if t is None:
+        return
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a dense {list(shape)} tensor of {' or '.join(map(str, dtypes))}, "
+                         f"got {list(t.shape)} of {t.dtype}" + ("" if t.is_contiguous() else ", not contiguous"))
+
+
+def _want_shards(name: str, ts, p: int, shape: tuple, *dtypes) -> None:
+    if ts is None:
+        return
+    if len(ts) != p:
+        raise ValueError(f"{name}: expected {p} shards, got {len(ts)}")
+    for i, t in enumerate(ts):
+        if t is None:
+            raise ValueError(f"{name}[{i}] is None")
+        _want(f"{name}[{i}]", t, shape, *dtypes)
+
+
+class _device_of:
+    """The tensors' device made current for a call (kernels launch on the current
+    device); ValueError if they are not all on it."""
+
+    def __init__(self, first, *more):
+        self.index = first.device.index if first.is_cuda else None
+        self.back = None
+        for m in more:
+            for t in (m if isinstance(m, (list, tuple)) else (m,)):
+                if t is not None and t.device != first.device:
+                    raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+
+    def __enter__(self):
+        if self.index is not None and self.index != torch.cuda.current_device():
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
 class Plan:
     """A tp_plan: block dimensions, shard count p, dtype, activation and the
     dtype of the full-shape partial sums (default: the plan dtype)."""
@@ -280,6 +324,25 @@ class Plan:
         check(lib.tp_vocab_cross_entropy(self._h, T, _arr(logits), _ptr(labels), float(grad_scale),
                                          _ptr(loss), _ptr(lse), _arr(dlogits), _stream(stream)),
               "tp_vocab_cross_entropy")
+
+    def vocab_linear_cross_entropy(self, T, X, W, labels, grad_scale, loss, lse=None, dX=None, dW=None,
+                                   chunk: int = 0, stream=None):
+        """tp_vocab_linear_cross_entropy: the output head X W^T (W: vocab shards) and its
+        softmax cross-entropy without the logits. dX / dW (both optional) receive the
+        gradients of grad_scale * sum(loss). chunk: tokens at a time (0: chosen)."""
+        if getattr(self, "vocab_padded", 0):
+            dt, shard = self.torch_dtype, (self.vocab_padded // self.p, self.hidden)
+            _want("X", X, (T, self.hidden), dt)
+            _want("dX", dX, (T, self.hidden), dt)
+            _want("labels", labels, (T,), torch.int32)
+            _want("loss", loss, (T,), torch.float32)
+            _want("lse", lse, (T,), torch.float32)
+            _want_shards("W", W, self.p, shard, dt)
+            _want_shards("dW", dW, self.p, shard, dt)
+        with _device_of(X, W, labels, loss, lse, dX, dW):
+            check(lib.tp_vocab_linear_cross_entropy(self._h, T, _ptr(X), _arr(W), _ptr(labels), float(grad_scale),
+                                                    _ptr(loss), _ptr(lse), _ptr(dX), _arr(dW), int(chunk),
+                                                    _stream(stream)), "tp_vocab_linear_cross_entropy")
 
     def describe(self) -> str:
         buf = ctypes.create_string_buffer(4096)
