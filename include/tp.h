@@ -332,6 +332,29 @@ TP_API tp_status tp_norm_sharded_fwd(tp_plan* plan, tp_norm_kind kind, int64_t r
                                      const void* const* beta, void* const* Y, float* mean,
                                      float* rstd, void* stream);
 
+/* The junction of two sublayers in one pass ([TP-blog] §3.3: statistics over
+ * the whole hidden dim): norms after a block and before the next one, fused with
+ * the block's gate and the scaled residual,
+ *   n = Norm_post(f);  x_out = res_scale * x + g * n;  y = Norm_pre(x_out).
+ *   x, f, x_out, y [rows, hidden] (x_out may alias x or f, for f only when no
+ *   backward follows). kind: LayerNorm (gamma, beta) or RMSNorm (beta ignored,
+ *   NULL ok), eps = 1e-5, fp32 statistics, biased variance in two exact passes.
+ *   gamma_post NULL: no norm after the block (n = f). gamma_pre NULL: none before
+ *   the next (y must be NULL). gate NULL: g = 1; else [gate_rows, hidden], token
+ *   row r using gate row r % gate_rows (1: a gate per channel; batch: a gate per
+ *   sequence of sequence-major tokens); rows % gate_rows must be 0.
+ *   x_out is rounded to the plan dtype first, and y is the norm of the rounded row.
+ *   stats (NULL ok when no backward follows): [4, rows] fp32, rows mean_post,
+ *   rstd_post, mean_pre, rstd_pre; the means are not written for RMSNorm, nor the
+ *   statistics of a norm that is absent.
+ * hidden a multiple of 8 and <= 16384 (bf16) or 8192 (fp32). */
+TP_API tp_status tp_gated_residual_norm_fwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, const void* x,
+                                            const void* f, float res_scale, const void* gate,
+                                            int64_t gate_rows, const void* gamma_post,
+                                            const void* beta_post, const void* gamma_pre,
+                                            const void* beta_pre, void* x_out, void* y, float* stats,
+                                            void* stream);
+
 /* Causal attention of each shard's local heads ([TP-blog] §3.1: full sequence,
  * whole heads, no cross-shard step). QKV[i] [seq*batch, 3*h/p] = [Q_i|K_i|V_i]
  * (the TP_QKV column output); O[i] [seq*batch, h/p] with head j of the shard
@@ -464,6 +487,24 @@ TP_API tp_status tp_norm_sharded_bwd(tp_plan* plan, tp_norm_kind kind, int64_t r
                                      const void* const* dY, const float* mean, const float* rstd,
                                      void* const* dX, float* const* dgamma, float* const* dbeta,
                                      void* stream);
+
+/* Backward of tp_gated_residual_norm_fwd, one pass over its rows: from the
+ * gradients dx_out of x_out and dy of y (either may be NULL: zero; dy must be NULL
+ * without a pre-norm), f, x_out and stats of the forward, dx and df [rows, hidden]
+ * (dx may alias dx_out, df may alias dy or f), and fp32 sums over rows, each NULL
+ * ok: dgate [gate_rows, hidden], dgamma_* and dbeta_* [hidden] (dbeta_* only for
+ * LayerNorm). f is read with a post-norm or a gate, x_out with a pre-norm (NULL ok
+ * otherwise; so is stats without any norm). The sums are deterministic. Uses the
+ * plan's workspace: make a call of the same sizes before capturing one.
+ * gate_rows <= 65534. With rows = 0 the sums are set to zero. */
+TP_API tp_status tp_gated_residual_norm_bwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, const void* f,
+                                            const void* x_out, const float* stats, const void* dx_out,
+                                            const void* dy, float res_scale, const void* gate,
+                                            int64_t gate_rows, const void* gamma_post,
+                                            const void* beta_post, const void* gamma_pre, void* dx,
+                                            void* df, float* dgate, float* dgamma_post,
+                                            float* dbeta_post, float* dgamma_pre, float* dbeta_pre,
+                                            void* stream);
 
 /* Attention backward of each shard's local heads ([TP-blog] §3.1: a shard's
  * attention touches only its own whole heads over the full sequence, so the

@@ -1369,6 +1369,129 @@ tp_status tp_norm_sharded_bwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, co
                                  rstd, plan->dtype, as_stream(stream));
 }
 
+// Checks shared by the junction's two passes.
+static tp_status check_gated_norm(const tp_plan* plan, tp_norm_kind kind, int64_t rows, const void* gate, int64_t gate_rows,
+                                  const void* gamma_post, const void* beta_post, const void* gamma_pre) {
+  TP_TRY(check_plan(plan));
+  TP_TRY(check_T(rows));
+  if (kind != TP_NORM_LAYER && kind != TP_NORM_RMS) return fail(TP_ERR_ARG, "unknown norm kind %d", kind);
+  const int h = plan->hidden;
+  if (h % 8) return fail(TP_ERR_UNSUPPORTED, "hidden = %d must be a multiple of 8", h);
+  const int hmax = plan->dtype == TP_BF16 ? 16384 : 8192;  // 2048 16-byte vectors a row
+  if (h > hmax) return fail(TP_ERR_UNSUPPORTED, "norms support hidden <= %d (got %d)", hmax, h);
+  if (gate) {
+    TP_TRY(check_ptr(gate, "gate"));
+    if (gate_rows < 1) return fail(TP_ERR_ARG, "gate_rows = %lld", static_cast<long long>(gate_rows));
+    if (rows % gate_rows)
+      return fail(TP_ERR_DIVISIBILITY, "rows = %lld is not divisible by gate_rows = %lld", static_cast<long long>(rows),
+                  static_cast<long long>(gate_rows));
+  }
+  if (gamma_post) {
+    TP_TRY(check_ptr(gamma_post, "gamma_post"));
+    if (kind == TP_NORM_LAYER) TP_TRY(check_ptr(beta_post, "beta_post"));
+  }
+  if (gamma_pre) TP_TRY(check_ptr(gamma_pre, "gamma_pre"));
+  return TP_OK;
+}
+
+tp_status tp_gated_residual_norm_fwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, const void* x, const void* f,
+                                     float res_scale, const void* gate, int64_t gate_rows, const void* gamma_post,
+                                     const void* beta_post, const void* gamma_pre, const void* beta_pre, void* x_out,
+                                     void* y, float* stats, void* stream) {
+  TP_TRY(check_gated_norm(plan, kind, rows, gate, gate_rows, gamma_post, beta_post, gamma_pre));
+  if (gamma_pre && kind == TP_NORM_LAYER) TP_TRY(check_ptr(beta_pre, "beta_pre"));
+  if (!gamma_pre && y) return fail(TP_ERR_ARG, "y must be NULL without a pre-norm");
+  if (rows == 0) return TP_OK;
+  TP_TRY(check_ptr(x, "x"));
+  TP_TRY(check_ptr(f, "f"));
+  TP_TRY(check_ptr(x_out, "x_out"));
+  if (gamma_pre) TP_TRY(check_ptr(y, "y"));
+  if (stats) TP_TRY(check_ptr(stats, "stats"));
+  if (y && (y == x_out || y == x || y == f)) return fail(TP_ERR_ARG, "y must not alias x, f or x_out");
+  GatedNorm p{};
+  p.x = x;
+  p.f = f;
+  p.gate = gate;
+  p.post_g = gamma_post;
+  p.post_b = beta_post;
+  p.pre_g = gamma_pre;
+  p.pre_b = beta_pre;
+  p.x_out = x_out;
+  p.y = y;
+  p.stats = stats;
+  p.rows = rows;
+  p.h = plan->hidden;
+  p.gate_rows = gate_rows;
+  p.rs = res_scale;
+  return launch_gated_norm_fwd(p, kind == TP_NORM_RMS, plan->dtype, as_stream(stream));
+}
+
+tp_status tp_gated_residual_norm_bwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, const void* f, const void* x_out,
+                                     const float* stats, const void* dx_out, const void* dy, float res_scale,
+                                     const void* gate, int64_t gate_rows, const void* gamma_post, const void* beta_post,
+                                     const void* gamma_pre, void* dx, void* df, float* dgate, float* dgamma_post,
+                                     float* dbeta_post, float* dgamma_pre, float* dbeta_pre, void* stream) {
+  TP_TRY(check_gated_norm(plan, kind, rows, gate, gate_rows, gamma_post, beta_post, gamma_pre));
+  const bool layer = kind == TP_NORM_LAYER;
+  if (!gamma_pre && dy) return fail(TP_ERR_ARG, "dy must be NULL without a pre-norm");
+  if (!gate && dgate) return fail(TP_ERR_ARG, "dgate without a gate");
+  if (gate && gate_rows > 65534)
+    return fail(TP_ERR_UNSUPPORTED, "gate_rows = %lld exceeds 65534", static_cast<long long>(gate_rows));
+  if (!gamma_post && (dgamma_post || dbeta_post)) return fail(TP_ERR_ARG, "post-norm gradients without a post-norm");
+  if (!gamma_pre && (dgamma_pre || dbeta_pre)) return fail(TP_ERR_ARG, "pre-norm gradients without a pre-norm");
+  if (!layer && (dbeta_post || dbeta_pre)) return fail(TP_ERR_ARG, "RMSNorm has no beta gradient");
+  float* sums[] = {dgate, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre};
+  const char* names[] = {"dgate", "dgamma_post", "dbeta_post", "dgamma_pre", "dbeta_pre"};
+  for (int i = 0; i < 5; ++i)
+    if (sums[i]) TP_TRY(check_ptr(sums[i], names[i]));
+  cudaStream_t st = as_stream(stream);
+  const bool pre = gamma_pre && dy;  // without dy the pre-norm passes nothing back
+  auto zero = [&](float* s, int64_t n) {
+    return s ? cuda_status(cudaMemsetAsync(s, 0, static_cast<size_t>(n) * plan->hidden * 4, st), "cudaMemsetAsync(sums)")
+             : TP_OK;
+  };
+  if (rows == 0) {
+    TP_TRY(zero(dgate, gate_rows));
+    for (int i = 1; i < 5; ++i) TP_TRY(zero(sums[i], 1));
+    return TP_OK;
+  }
+  if (!dx_out && !dy) return fail(TP_ERR_ARG, "dx_out and dy are both NULL");
+  if (dx_out) TP_TRY(check_ptr(dx_out, "dx_out"));
+  if (dy) TP_TRY(check_ptr(dy, "dy"));
+  if (gamma_post || gate) TP_TRY(check_ptr(f, "f"));
+  if (pre) TP_TRY(check_ptr(x_out, "x_out"));
+  if (gamma_post || pre) TP_TRY(check_ptr(stats, "stats"));
+  TP_TRY(check_ptr(dx, "dx"));
+  TP_TRY(check_ptr(df, "df"));
+  if (dx == df) return fail(TP_ERR_ARG, "dx and df must not alias");
+  if (gamma_pre && !pre) {
+    TP_TRY(zero(dgamma_pre, 1));
+    TP_TRY(zero(dbeta_pre, 1));
+  }
+  GatedNorm p{};
+  p.f = f;
+  p.gate = gate;
+  p.post_g = gamma_post;
+  p.post_b = beta_post;
+  p.pre_g = pre ? gamma_pre : nullptr;
+  p.x_in = x_out;
+  p.dx_out = dx_out;
+  p.dy = dy;
+  p.dx = dx;
+  p.df = df;
+  p.stats = const_cast<float*>(stats);
+  p.dgate = dgate;
+  p.dpost_g = dgamma_post;
+  p.dpost_b = dbeta_post;
+  p.dpre_g = pre ? dgamma_pre : nullptr;
+  p.dpre_b = pre ? dbeta_pre : nullptr;
+  p.rows = rows;
+  p.h = plan->hidden;
+  p.gate_rows = gate_rows;
+  p.rs = res_scale;
+  return launch_gated_norm_bwd(plan, p, !layer, plan->dtype, st);
+}
+
 tp_status tp_column_sum(tp_plan* plan, int64_t rows, int64_t cols, const void* x, float* out,
                         int accumulate, void* stream) {
   TP_TRY(check_plan(plan));

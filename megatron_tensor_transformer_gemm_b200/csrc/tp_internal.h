@@ -188,6 +188,20 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
                                  const int32_t* labels, float scale, float* loss, float* lse, void* dX,
                                  const MutPtrArray& dW, int64_t chunk, cudaStream_t st);
 
+// The junction of two sublayers (tp_gated_norm.cu): pointers as in
+// tp_gated_residual_norm_fwd / _bwd, NULL where absent; x_in is the backward's
+// x_out. The launchers set seg and cta_part.
+struct GatedNorm {
+  const void *x, *f, *gate, *post_g, *post_b, *pre_g, *pre_b, *x_in, *dx_out, *dy;
+  void *x_out, *y, *dx, *df;
+  float *stats, *dgate, *dpost_g, *dpost_b, *dpre_g, *dpre_b;
+  float *seg, *cta_part;
+  int64_t rows, h, gate_rows;
+  float rs;
+};
+tp_status launch_gated_norm_fwd(const GatedNorm& p, bool rms, tp_dtype dt, cudaStream_t st);
+tp_status launch_gated_norm_bwd(tp_plan* plan, const GatedNorm& p, bool rms, tp_dtype dt, cudaStream_t st);
+
 // Norms of hidden-sharded rows (tp_layernorm.cu).
 tp_status launch_norm_sharded_fwd(bool rms, const PtrArray& X, const PtrArray& G,
                                   const PtrArray& B, const MutPtrArray& Y, int p, int64_t rows,

@@ -99,6 +99,10 @@ _SIGS = {
     "tp_vocab_cross_entropy": (_int, [_plan_p, _i64, _vpp, _vp, ctypes.c_float, _fp, _fp, _vpp, _vp]),
     "tp_vocab_linear_cross_entropy": (_int, [_plan_p, _i64, _vp, _vpp, _vp, ctypes.c_float, _fp, _fp, _vp, _vpp,
                                              _i64, _vp]),
+    "tp_gated_residual_norm_fwd": (_int, [_plan_p, _int, _i64, _vp, _vp, ctypes.c_float, _vp, _i64] + [_vp] * 7
+                                   + [_vp]),
+    "tp_gated_residual_norm_bwd": (_int, [_plan_p, _int, _i64, _vp, _vp, _fp, _vp, _vp, ctypes.c_float, _vp, _i64]
+                                   + [_vp] * 10 + [_vp]),
     "tp_norm_sharded_fwd": (_int, [_plan_p, _int, _i64, _vpp, _vpp, _vpp, _vpp, _fp, _fp, _vp]),
     "tp_norm_sharded_bwd": (_int, [_plan_p, _int, _i64, _vpp, _vpp, _vpp, _fp, _fp, _vpp, _vpp, _vpp, _vp]),
     "tp_row_fwd_reduce": (_int, [_plan_p, _int, _i64, _vpp, _vpp, _vp, _vp, _vp, _vp]),
@@ -422,6 +426,40 @@ class Plan:
                                       _ptr(mean), _ptr(rstd), _arr(dX), _arr(dgamma), _arr(dbeta),
                                       _stream(stream)), "tp_norm_sharded_bwd")
 
+    def _check_junction(self, kind, rows, rows_of, weights, gate, dgate=None, sums=()):
+        h, dt = self.hidden, self.torch_dtype
+        for name, t in rows_of:
+            _want(name, t, (rows, h), dt)
+        for name, pair in weights:
+            if pair is not None and kind == "layer" and pair[1] is None:
+                raise ValueError(f"{name}: LayerNorm needs (gamma, beta)")
+            for t in pair or ():
+                _want(name, t, (h,), dt)
+        for name, pair in sums:
+            for t in pair or ():
+                _want(name, t, (h,), torch.float32)
+        if gate is not None:
+            if gate.dim() != 2:
+                raise ValueError(f"gate: expected [gate_rows, {h}], got {list(gate.shape)}")
+            _want("gate", gate, (gate.shape[0], h), dt)
+            _want("dgate", dgate, (gate.shape[0], h), torch.float32)
+
+    def gated_residual_norm_fwd(self, kind, rows, x, f, x_out, y=None, *, res_scale=1.0, gate=None, post=None,
+                                pre=None, stats=None, stream=None):
+        """tp_gated_residual_norm_fwd: x_out = res_scale * x + gate * Norm_post(f), y = Norm_pre(x_out).
+        kind: "layer" or "rms"; post, pre: (gamma, beta) or None (beta may be None for "rms");
+        gate [gate_rows, hidden]; stats [4, rows] fp32, kept for the backward."""
+        self._check_junction(kind, rows, (("x", x), ("f", f), ("x_out", x_out), ("y", y)),
+                             (("post", post), ("pre", pre)), gate)
+        _want("stats", stats, (4, rows), torch.float32)
+        pg, pb = post if post else (None, None)
+        qg, qb = pre if pre else (None, None)
+        with _device_of(x, f, x_out, y, gate, pg, pb, qg, qb, stats):
+            check(lib.tp_gated_residual_norm_fwd(
+                self._h, NORMS[kind], rows, _ptr(x), _ptr(f), float(res_scale), _ptr(gate),
+                0 if gate is None else gate.shape[0], _ptr(pg), _ptr(pb), _ptr(qg), _ptr(qb), _ptr(x_out), _ptr(y),
+                _ptr(stats), _stream(stream)), "tp_gated_residual_norm_fwd")
+
     def attention_fwd(self, batch, seq, QKV, O, LSE=None, stream=None):
         check(lib.tp_attention_fwd(self._h, batch, seq, _arr(QKV), _arr(O), _arr(LSE),
                                    _stream(stream)), "tp_attention_fwd")
@@ -474,6 +512,26 @@ class Plan:
         check(lib.tp_layernorm_bwd(self._h, rows, _ptr(x), _ptr(gamma), _ptr(dy), _ptr(mean),
                                    _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
                                    1 if accumulate else 0, _stream(stream)), "tp_layernorm_bwd")
+
+    def gated_residual_norm_bwd(self, kind, rows, f, x_out, stats, dx_out, dy, dx, df, *, res_scale=1.0, gate=None,
+                                dgate=None, post=None, dpost=None, pre=None, dpre=None, stream=None):
+        """tp_gated_residual_norm_bwd: dx and df from dx_out and dy (either may be None), with
+        dgate, dpost = (dgamma, dbeta) and dpre as fp32 sums over rows (each optional)."""
+        self._check_junction(kind, rows, (("f", f), ("x_out", x_out), ("dx_out", dx_out), ("dy", dy), ("dx", dx), ("df", df)),
+                             (("post", post), ("pre", pre)), gate, dgate, (("dpost", dpost), ("dpre", dpre)))
+        _want("stats", stats, (4, rows), torch.float32)
+        pg, pb = post if post else (None, None)
+        qg = pre[0] if pre else None
+        dpg, dpb = dpost if dpost else (None, None)
+        dqg, dqb = dpre if dpre else (None, None)
+        if kind == "rms":
+            dpb = dqb = None
+        with _device_of(dx, f, x_out, stats, dx_out, dy, df, gate, dgate, pg, pb, qg, dpg, dpb, dqg, dqb):
+            check(lib.tp_gated_residual_norm_bwd(
+                self._h, NORMS[kind], rows, _ptr(f), _ptr(x_out), _ptr(stats), _ptr(dx_out), _ptr(dy), float(res_scale),
+                _ptr(gate), 0 if gate is None else gate.shape[0], _ptr(pg), _ptr(pb), _ptr(qg), _ptr(dx), _ptr(df),
+                _ptr(dgate), _ptr(dpg), _ptr(dpb), _ptr(dqg), _ptr(dqb), _stream(stream)),
+                "tp_gated_residual_norm_bwd")
 
     def attention_bwd(self, batch, seq, QKV, O, dO, LSE, dQKV, stream=None):
         check(lib.tp_attention_bwd(self._h, batch, seq, _arr(QKV), _arr(O), _arr(dO), _arr(LSE),

@@ -59,3 +59,60 @@ def test_loss_binding_checks_shapes_types_and_strides(head):
         call(4, X, W[:1], lab, 1.0, loss)
     with pytest.raises(ValueError, match=r"dW\[1\]"):
         call(4, X, W, lab, 1.0, loss, dW=[W[0].clone(), W[1][:8].clone()])
+
+
+def _fwd(plan, kind=0, rows=8, x=A, f=A + 16, gate=None, gate_rows=0, pg=A, pb=A, qg=A, qb=A, xo=A + 32, y=A + 48, stats=None):
+    return tp.lib.tp_gated_residual_norm_fwd(plan.handle, kind, rows, x, f, 1.0, gate, gate_rows, pg, pb, qg, qb, xo, y, stats, None)
+
+
+def _bwd(plan, kind=0, rows=8, f=A, xo=A, stats=A, dxo=A, dy=A, gate=None, gate_rows=0, pg=A, pb=A, qg=A, dx=A + 16, df=A + 32,
+         dgate=None, dpg=None, dpb=None, dqg=None, dqb=None):
+    return tp.lib.tp_gated_residual_norm_bwd(plan.handle, kind, rows, f, xo, stats, dxo, dy, 1.0, gate, gate_rows, pg, pb, qg,
+                                             dx, df, dgate, dpg, dpb, dqg, dqb, None)
+
+
+def test_gated_norm_refusals():
+    plan = tp.Plan(64, 0, 0, 1, "bf16", "none")
+    assert _fwd(plan, kind=2) == 1 and "kind" in tp.last_error()
+    assert _fwd(plan, rows=-1) == 1
+    assert _fwd(plan, x=None) == 1 and _fwd(plan, f=A + 2) == 3 and _fwd(plan, xo=None) == 1
+    assert _fwd(plan, y=None) == 1 and "y" in tp.last_error()
+    assert _fwd(plan, qg=None) == 1 and "pre-norm" in tp.last_error()
+    assert _fwd(plan, pb=None) == 1 and "beta_post" in tp.last_error()
+    assert _fwd(plan, qb=None) == 1 and "beta_pre" in tp.last_error()
+    assert _fwd(plan, y=A + 32) == 1 and "alias" in tp.last_error()
+    assert _fwd(plan, stats=A + 4) == 3
+    assert _fwd(plan, gate=A, gate_rows=0) == 1 and "gate_rows" in tp.last_error()
+    assert _fwd(plan, gate=A, gate_rows=3) == 2 and "gate_rows = 3" in tp.last_error()
+    assert _fwd(plan, rows=0, x=None, f=None, xo=None, y=None) == 0
+    assert _fwd(tp.Plan(60, 0, 0, 1, "f32", "none")) == 5
+    assert _fwd(tp.Plan(8200, 0, 0, 1, "f32", "none")) == 5 and "hidden <= 8192" in tp.last_error()
+    assert _bwd(plan, dxo=None, dy=None) == 1 and "both NULL" in tp.last_error()
+    assert _bwd(plan, qg=None) == 1 and "pre-norm" in tp.last_error()
+    assert _bwd(plan, dgate=A) == 1 and "gate" in tp.last_error()
+    assert _bwd(plan, pg=None, dpg=A) == 1 and _bwd(plan, qg=None, dy=None, dqg=A) == 1
+    assert _bwd(plan, kind=1, dpb=A) == 1 and "RMSNorm" in tp.last_error()
+    assert _bwd(plan, f=None) == 1 and _bwd(plan, xo=None) == 1 and _bwd(plan, stats=None) == 1
+    assert _bwd(plan, dx=None) == 1 and _bwd(plan, df=A + 16) == 1 and "alias" in tp.last_error()
+    assert _bwd(plan, rows=131072, gate=A, gate_rows=65536) == 5
+    assert _bwd(plan, dqg=A + 4) == 3
+    assert _bwd(plan, rows=0, f=None, xo=None, stats=None, dxo=None, dy=None, dx=None, df=None) == 0
+
+
+def test_gated_norm_binding_checks():
+    plan = tp.Plan(64, 0, 0, 1, "bf16", "none")
+    x = torch.zeros(8, 64).bfloat16()
+    w = torch.ones(64).bfloat16()
+    call = plan.gated_residual_norm_fwd
+    with pytest.raises(ValueError, match="x_out"):
+        call("layer", 8, x, x, x.float())
+    with pytest.raises(ValueError, match="post"):
+        call("layer", 8, x, x, x, post=(w, None))
+    with pytest.raises(ValueError, match="post"):
+        call("layer", 8, x, x, x, post=(w.float(), w))
+    with pytest.raises(ValueError, match="gate"):
+        call("layer", 8, x, x, x, gate=w)
+    with pytest.raises(ValueError, match="stats"):
+        call("layer", 8, x, x, x, stats=torch.zeros(2, 8))
+    with pytest.raises(KeyError):
+        call("batch", 8, x, x, x)
