@@ -198,6 +198,23 @@ TP_API tp_status tp_column_fwd(tp_plan* plan, tp_which which, int64_t T, const v
                         const void* const* W, const void* const* bias, void* const* Z,
                         void* const* H, void* stream);
 
+/* The MLP's column layer keeping its pre-activation in 8 bits for the backward
+ * (an activation checkpoint of 1.03 bytes an element in place of the 2 of Z and
+ * the 2 of H, which tp_row_bwd_ckpt8 computes again): as tp_column_fwd with
+ * TP_MLP (GELU with an optional bias, or SwiGLU), with Z written as
+ *   Zq[i] [T, n1]      e4m3 codes (n1 = ffn/p, or 2*ffn/p = [gate | up] for SwiGLU),
+ *   Zs[i] [groups, T]  one byte per 32 columns of a row, the biased exponent of a
+ *                      power of two (e8m0): Z = code * 2^(Zs - 127).
+ * Groups of each half start anew: groups = ceil(ffn/p / 32), twice that for
+ * SwiGLU. The scale is the least power of two, at least 2^-126, that brings the
+ * group's largest magnitude to at most 448; codes are rounded to nearest, so a
+ * value is off by at most 2^-4 of itself, or 2^-10 of the scale where it is small.
+ * H[i] [T, ffn/p] is the activation of the unrounded Z. bf16 plans; ffn/p a
+ * multiple of 16 (TP_ERR_ALIGN). */
+TP_API tp_status tp_column_fwd_ckpt8(tp_plan* plan, int64_t T, const void* X, const void* const* W,
+                                     const void* const* bias, void* const* Zq, uint8_t* const* Zs,
+                                     void* const* H, void* stream);
+
 /* Row-parallel GEMM of every shard: P[i] [T, hidden] = H[i] W[i]^T, the
  * full-shape partial sums, with NO bias ([TP-blog] §2.2, [TP-wiki] XB = X_1B_1 +
  * X_2B_2). H[i] is [T, ffn/p] (TP_MLP) or [T, h/p] (TP_OUTPROJ); W[i] the row
@@ -420,6 +437,16 @@ TP_API tp_status tp_flush_wgrad(tp_plan* plan);
 TP_API tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void* dY,
                      const void* const* H, const void* const* W, const void* const* Z,
                      void* const* dZ, void* const* dW, float* dbias, void* stream);
+
+/* tp_row_bwd of the MLP from the pre-activation kept by tp_column_fwd_ckpt8:
+ * with Z decoded from Zq and Zs in the GEMM's epilogue, dZ[i] as in tp_row_bwd,
+ * H[i] [T, ffn/p] = the activation of the decoded Z (NULL array skips when dW is
+ * NULL), dW[i] = dY^T H[i] with that H, and dbias. Everything runs on `stream`
+ * (the deferred and grouped modes do not apply; a waiting weight gradient is
+ * launched first). With T = 0, dW and dbias are set to zero. */
+TP_API tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void* const* W,
+                                  const void* const* Zq, const uint8_t* const* Zs, void* const* H,
+                                  void* const* dZ, void* const* dW, float* dbias, void* stream);
 
 /* Column layer backward for every shard ([TP-scratch] §四: forward identity,
  * backward sum of the input gradient).

@@ -132,6 +132,32 @@ tp_status device_status_word(unsigned** out) {
   return TP_OK;
 }
 
+void note_capture(tp_plan* plan, cudaStream_t st) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
+    cudaGetLastError();
+    return;
+  }
+  if (cs != cudaStreamCaptureStatusNone) plan->captured = 1;
+}
+
+// Let go of a workspace block that a larger one replaces: freed once the
+// device's work is done, or, when graphs captured from this plan may replay
+// with its address, kept until the plan is destroyed.
+static tp_status release_block(tp_plan* plan, void* p, int device, int cur) {
+  if (plan->captured) {
+    Retired* r = new (std::nothrow) Retired{p, device, plan->retired};
+    if (!r) return fail(TP_ERR_ARG, "out of host memory for the plan's workspace");
+    plan->retired = r;
+    return TP_OK;
+  }
+  if (device != cur) cudaSetDevice(device);
+  cudaDeviceSynchronize();
+  cudaFree(p);
+  if (device != cur) cudaSetDevice(cur);
+  return TP_OK;
+}
+
 tp_status workspace(tp_plan* plan, size_t bytes, void** out) {
   int dev = 0;
   tp_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
@@ -139,11 +165,7 @@ tp_status workspace(tp_plan* plan, size_t bytes, void** out) {
   if (plan->ws && (plan->ws_bytes < bytes || plan->ws_device != dev)) {
     // Grow (or move to another device): release the old block first. The
     // caller's stream may still use it, so wait for the device.
-    cudaDeviceSynchronize();
-    int cur = dev;
-    if (plan->ws_device != dev) cudaSetDevice(plan->ws_device);
-    cudaFree(plan->ws);
-    if (plan->ws_device != dev) cudaSetDevice(cur);
+    TP_TRY(release_block(plan, plan->ws, plan->ws_device, dev));
     plan->ws = nullptr;
     plan->ws_bytes = 0;
   }
@@ -202,11 +224,7 @@ tp_status workspace2(tp_plan* plan, size_t bytes, void** out) {
   tp_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
   if (s != TP_OK) return s;
   if (plan->ws2 && (plan->ws2_bytes < bytes || plan->ws2_device != dev)) {
-    cudaDeviceSynchronize();  // side-stream work may still use the old block
-    int cur = dev;
-    if (plan->ws2_device != dev) cudaSetDevice(plan->ws2_device);
-    cudaFree(plan->ws2);
-    if (plan->ws2_device != dev) cudaSetDevice(cur);
+    TP_TRY(release_block(plan, plan->ws2, plan->ws2_device, dev));  // side-stream work may still use it
     plan->ws2 = nullptr;
     plan->ws2_bytes = 0;
   }
@@ -234,20 +252,9 @@ tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out) {
     if (capturing)
       return fail(TP_ERR_ARG, "the plan's workspace must grow to %zu bytes: make the call once before the stream capture",
                   bytes);
-    if (plan->sc && plan->sc_captured) {
-      Retired* r = new (std::nothrow) Retired{plan->sc, plan->sc_device, plan->sc_retired};
-      if (!r) return fail(TP_ERR_ARG, "out of host memory for the plan's workspace");
-      plan->sc_retired = r;
-    } else if (plan->sc) {
-      // an earlier call may still use the block, on any stream of its device
-      if (plan->sc_device != dev) cudaSetDevice(plan->sc_device);
-      cudaDeviceSynchronize();
-      cudaFree(plan->sc);
-      if (plan->sc_device != dev) cudaSetDevice(dev);
-    }
+    if (plan->sc) TP_TRY(release_block(plan, plan->sc, plan->sc_device, dev));
     plan->sc = nullptr;
     plan->sc_bytes = 0;
-    plan->sc_captured = 0;
     const size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
     void* p = nullptr;
     TP_TRY(cuda_status(cudaMalloc(&p, want), "cudaMalloc(scratch)"));
@@ -255,7 +262,7 @@ tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out) {
     plan->sc_bytes = want;
     plan->sc_device = dev;
   }
-  if (capturing) plan->sc_captured = 1;
+  if (capturing) plan->captured = 1;
   *out = plan->sc;
   return TP_OK;
 }
@@ -628,9 +635,9 @@ void tp_plan_destroy(tp_plan* plan) {
     cudaDeviceSynchronize();
     cudaFree(plan->sc);
   }
-  while (plan->sc_retired) {
-    tpi::Retired* r = plan->sc_retired;
-    plan->sc_retired = r->next;
+  while (plan->retired) {
+    tpi::Retired* r = plan->retired;
+    plan->retired = r->next;
     cudaSetDevice(r->device);
     cudaDeviceSynchronize();
     cudaFree(r->p);
@@ -1213,6 +1220,7 @@ tp_status tp_layernorm_bwd(tp_plan* plan, int64_t rows, const void* x, const voi
   TP_TRY(check_ptr(dbeta, "dbeta"));
   if (dres) TP_TRY(check_ptr(dres, "dres"));
   TP_TRY(check_ln(plan));
+  note_capture(plan, as_stream(stream));
   return launch_layernorm_bwd(plan, x, gamma, dy, mean, rstd, dres, dx, dgamma, dbeta, accumulate,
                               rows, plan->hidden, plan->dtype, as_stream(stream));
 }
@@ -1260,6 +1268,7 @@ tp_status tp_embedding_bwd(tp_plan* plan, int64_t T, const int32_t* ids, const v
   size_t bytes = 0;
   TP_TRY(embedding_bwd_workspace(T, plan->vocab_padded, &bytes));
   void* ws = nullptr;
+  note_capture(plan, as_stream(stream));
   TP_TRY(workspace(plan, bytes, &ws));
   return launch_embedding_bwd(ids, T, dY, plan->hidden, plan->vocab, plan->vocab_padded,
                               plan->vocab_padded / p, to_marr(dE, p), plan->dtype, ws,
@@ -1364,6 +1373,7 @@ tp_status tp_norm_sharded_bwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, co
     dg.p[i] = dgamma[i];
     db.p[i] = dbeta ? dbeta[i] : nullptr;
   }
+  note_capture(plan, as_stream(stream));
   return launch_norm_sharded_bwd(plan, kind == TP_NORM_RMS, to_arr(X, p), to_arr(gamma, p),
                                  to_arr(dY, p), to_marr(dX, p), dg, db, p, rows, plan->hidden, mean,
                                  rstd, plan->dtype, as_stream(stream));
@@ -1500,6 +1510,7 @@ tp_status tp_column_sum(tp_plan* plan, int64_t rows, int64_t cols, const void* x
   if (rows > 0) TP_TRY(check_ptr(x, "x"));
   TP_TRY(check_ptr(out, "out"));
   TP_TRY(check_row_bytes(cols, plan->dtype, "cols"));
+  note_capture(plan, as_stream(stream));
   return launch_column_sum(plan, x, rows, cols, cols, out, accumulate, plan->dtype,
                            as_stream(stream));
 }
@@ -1535,6 +1546,7 @@ tp_status tp_attention_bwd(tp_plan* plan, int batch, int seq, const void* const*
   TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dQKV), p, "dQKV", false));
   if (plan->head_dim != 64 && plan->head_dim != 128)
     return fail(TP_ERR_UNSUPPORTED, "attention supports head_dim 64 or 128 (got %d)", plan->head_dim);
+  note_capture(plan, as_stream(stream));
   return launch_attention_bwd(plan, batch, seq, to_arr(QKV, p), to_arr(O, p), to_arr(dO, p), LSE,
                               to_marr(dQKV, p), as_stream(stream));
 }
@@ -1562,6 +1574,7 @@ tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void* dY,
   TP_TRY(check_row_bytes(h, plan->dtype, "hidden"));
   if (T == 0) return TP_OK;
   cudaStream_t st = as_stream(stream);
+  note_capture(plan, st);
 
   // dH_i = dY W_i (W_i is [h, k]: (n = j, k = c) at W_i + c*k + j -> MN-major B),
   // with the activation derivative fused in the epilogue.
@@ -1670,6 +1683,7 @@ static tp_status column_bwd_common(tp_plan* plan, tp_which which, int64_t T, con
   TP_TRY(check_row_bytes(h, plan->dtype, "hidden"));
   if (mode == 0) TP_TRY(check_row_bytes(h, plan->partial_dtype, "hidden (dX partials)"));
   if (T == 0) return TP_OK;
+  note_capture(plan, st);
   GemmBatch w{};
   if (dW) {
     // dW_i [n, h] = dZ_i^T X: A(m, t) = dZ_i[t, m] (MN-major), B(c, t) = X[t, c] (MN-major).
@@ -1752,6 +1766,140 @@ static tp_status column_bwd_common(tp_plan* plan, tp_which which, int64_t T, con
   else TP_TRY(flush_wgrad(plan));
   if (has_dx && !side) TP_TRY(run_gemm(plan, d, st));
   return TP_OK;
+}
+
+// ------------------------------------------- 8-bit activation checkpoints
+
+// Checks shared by the two passes; *k = ffn / p.
+static tp_status check_ckpt8(const tp_plan* plan, int64_t T, int* k) {
+  TP_TRY(check_plan(plan));
+  TP_TRY(check_T(T));
+  TP_TRY(row_k(plan, TP_MLP, k));
+  if (plan->dtype != TP_BF16) return fail(TP_ERR_DTYPE, "8-bit activation checkpoints need a bf16 plan");
+  if (plan->act == TP_ACT_NONE) return fail(TP_ERR_ARG, "the plan's MLP has no activation: there is no pre-activation to keep");
+  if (*k % 16) return fail(TP_ERR_ALIGN, "ffn/p = %d: rows of 8-bit values must be multiples of 16 bytes", *k);
+  TP_TRY(check_row_bytes(plan->hidden, plan->dtype, "hidden"));
+  return TP_OK;
+}
+// The scales are bytes: one per token and group, of any alignment.
+static tp_status check_scales(const uint8_t* const* s, int p) {
+  if (!s) return fail(TP_ERR_ARG, "Zs (pointer array) is NULL");
+  for (int i = 0; i < p; ++i)
+    if (!s[i]) return fail(TP_ERR_ARG, "Zs[%d] is NULL", i);
+  return TP_OK;
+}
+
+tp_status tp_column_fwd_ckpt8(tp_plan* plan, int64_t T, const void* X, const void* const* W, const void* const* bias,
+                              void* const* Zq, uint8_t* const* Zs, void* const* H, void* stream) {
+  int k = 0;
+  TP_TRY(check_ckpt8(plan, T, &k));
+  const int p = plan->p, h = plan->hidden;
+  const bool swiglu = plan->act == TP_ACT_SWIGLU;
+  TP_TRY(check_ptrs(W, p, "W", false));
+  TP_TRY(check_ptrs(bias, p, "bias", true));
+  if (swiglu && bias) return fail(TP_ERR_ARG, "a column bias is not supported with SwiGLU");
+  if (T == 0) return TP_OK;
+  TP_TRY(check_ptr(X, "X"));
+  TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(Zq), p, "Zq", false));
+  TP_TRY(check_scales(Zs, p));
+  TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(H), p, "H", false));
+  GemmBatch b{};
+  b.n = p;
+  b.epi = swiglu ? EPI_SWIGLU : EPI_BIAS_GELU;
+  for (int i = 0; i < p; ++i) {
+    GemmProblem& g = b.g[i];
+    g.M = static_cast<int>(T);
+    g.N = k;
+    g.K = h;
+    g.A = X;
+    g.lda = h;
+    g.B = W[i];
+    g.ldb = h;
+    g.bias = bias ? bias[i] : nullptr;
+    g.D2 = H[i];
+    g.ldd2 = k;
+    g.nh = k;
+    g.q = static_cast<uint8_t*>(Zq[i]);
+    g.ldq = swiglu ? 2 * k : k;
+    g.qs = Zs[i];
+    g.lds = T;
+  }
+  return launch_gemm_bf16(b, as_stream(stream));
+}
+
+tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void* const* W, const void* const* Zq,
+                           const uint8_t* const* Zs, void* const* H, void* const* dZ, void* const* dW, float* dbias,
+                           void* stream) {
+  int k = 0;
+  TP_TRY(check_ckpt8(plan, T, &k));
+  const int p = plan->p, h = plan->hidden;
+  const bool swiglu = plan->act == TP_ACT_SWIGLU;
+  const int nz = swiglu ? 2 * k : k;
+  TP_TRY(check_ptrs(W, p, "W", false));
+  TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dW), p, "dW", true));
+  if (dbias) TP_TRY(check_ptr(dbias, "dbias"));
+  if (dW && !H) return fail(TP_ERR_ARG, "dW needs H, which it is the product with");
+  cudaStream_t st = as_stream(stream);
+  TP_TRY(flush_wgrad(plan));
+  if (T == 0) {  // sums over no token
+    for (int i = 0; dW && i < p; ++i)
+      TP_TRY(cuda_status(cudaMemsetAsync(dW[i], 0, static_cast<size_t>(h) * k * 2, st), "cudaMemsetAsync(dW)"));
+    if (dbias) TP_TRY(cuda_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(h) * 4, st), "cudaMemsetAsync(dbias)"));
+    return TP_OK;
+  }
+  TP_TRY(check_ptr(dY, "dY"));
+  TP_TRY(check_ptrs(Zq, p, "Zq", false));
+  TP_TRY(check_scales(Zs, p));
+  TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(H), p, "H", true));
+  TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dZ), p, "dZ", false));
+  note_capture(plan, st);
+  GemmBatch b{};
+  b.n = p;
+  b.b_mn = true;
+  b.epi = swiglu ? EPI_DSWIGLU_Q : EPI_DGELU_Q;
+  GemmBatch w{};
+  w.n = p;
+  w.a_mn = w.b_mn = true;
+  w.epi = EPI_STORE;
+  for (int i = 0; i < p; ++i) {
+    GemmProblem& g = b.g[i];  // dH_i = dY W_i, as in tp_row_bwd
+    g.M = static_cast<int>(T);
+    g.N = k;
+    g.K = h;
+    g.A = dY;
+    g.lda = h;
+    g.B = W[i];
+    g.ldb = k;
+    g.D = dZ[i];
+    g.ldd = nz;
+    g.D2 = H ? H[i] : nullptr;
+    g.ldd2 = k;
+    g.nh = k;
+    g.q = static_cast<uint8_t*>(const_cast<void*>(Zq[i]));
+    g.ldq = nz;
+    g.qs = const_cast<uint8_t*>(Zs[i]);
+    g.lds = T;
+    if (dW) {
+      GemmProblem& o = w.g[i];  // dW_i = dY^T H_i
+      o.M = h;
+      o.N = k;
+      o.K = static_cast<int>(T);
+      o.A = dY;
+      o.lda = h;
+      o.B = H[i];
+      o.ldb = k;
+      o.D = dW[i];
+      o.ldd = k;
+    }
+  }
+  TP_TRY(launch_gemm_bf16(b, st));
+  if (dbias) TP_TRY(launch_column_sum(plan, dY, T, h, h, dbias, 0, plan->dtype, st));
+  if (!dW) return TP_OK;
+  const int s = gemm_split_k(w);
+  if (s <= 1) return launch_gemm_bf16(w, st);
+  void* part = nullptr;
+  TP_TRY(scratch(plan, static_cast<size_t>(s) * p * h * k * sizeof(float), st, &part));
+  return launch_gemm_split(w, s, static_cast<float*>(part), st);
 }
 
 tp_status tp_column_bwd(tp_plan* plan, tp_which which, int64_t T, const void* X,

@@ -490,4 +490,53 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
+// 8-bit groups: 32 values as e4m3 codes times one power of two, the least (at
+// least 2^-126) that brings their largest magnitude to at most 448, the format's
+// largest: no value saturates, and a power of two adds no rounding of its own,
+// so a normal code is off by at most 2^-4 of its value. 448 = 1.75 * 2^8: adding
+// 0x1fffff to the bits of the largest magnitude carries into the exponent
+// exactly when its significand is above 1.75. A NaN keeps its place as a NaN
+// code; an infinity decodes to one (its group's other values to zero).
+__device__ __forceinline__ uint32_t group_exponent(const float (&v)[32]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) m = max3(m, fabsf(v[i]), fabsf(v[i + 1]));
+  const int e = static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 8;
+  return static_cast<uint32_t>(e < 1 ? 1 : e);  // biased by 127
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+// Codes of 32 values at biased exponent e, 16 bytes each half.
+__device__ __forceinline__ void group_encode(const float (&v)[32], uint32_t e, uint4 (&q)[2]) {
+  const float inv = __uint_as_float((254u - e) << 23);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+  q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t u) {
+  uint32_t h;  // every e4m3 value is an f16 value
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(u));
+  float2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h));
+  return r;
+}
+__device__ __forceinline__ void group_decode(const uint4 (&q)[2], uint32_t e, float (&v)[32]) {
+  const float scale = __uint_as_float(e ? e << 23 : 0x400000u);
+  const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 a = e4m3x2_to_f32(static_cast<uint16_t>(w[i])), b = e4m3x2_to_f32(static_cast<uint16_t>(w[i] >> 16));
+    v[4 * i] = a.x * scale; v[4 * i + 1] = a.y * scale; v[4 * i + 2] = b.x * scale; v[4 * i + 3] = b.y * scale;
+  }
+}
+
 }  // namespace tpd

@@ -8,6 +8,8 @@
 //   EPI_SWIGLU     Z = [g|u], H = SiLU(g) * u            column layer, SwiGLU MLP
 //   EPI_DGELU      dZ = acc * GELU'(Z)                   row layer backward
 //   EPI_DSWIGLU    dZ = [acc*u*SiLU'(g) | acc*SiLU(g)]   row layer backward
+//   EPI_DGELU_Q / EPI_DSWIGLU_Q: the same from Z kept in 8 bits (which
+//   EPI_BIAS_GELU / EPI_SWIGLU may write instead of Z), with H computed again
 // (TP walkthrough 2kiu.com §2.1-§2.2 and §3.2; 张量并行 wiki, 两种切法.)
 //
 // Tile layouts: a CTA pair (cta_group::2) on a 256 x 256 tile by default; for
@@ -89,6 +91,10 @@ struct GroupArgs {
   int64_t ldaux;
   const float* acc;
   int64_t ldacc;
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* qs;
+  int64_t lds;
 };
 
 struct alignas(64) GemmParams {
@@ -223,6 +229,65 @@ __device__ __forceinline__ void load_row_chunk_bf16(const void* base, int64_t ld
   }
 }
 
+// ------------------------------------------- 8-bit pre-activations
+// A thread owns one row's 32 columns of a chunk, which is one scale group, so
+// the group's largest magnitude needs no exchange; the codes leave as the row's
+// one or two 16-byte pieces (one 32-byte sector), and a warp's 32 scale bytes of
+// a group are adjacent in the group-major layout.
+struct QGroup {
+  uint4 q[2];
+  uint32_t e;
+};
+// Half hf's (gate 0, up 1) group at column j0 of row `row`.
+__device__ __forceinline__ uint8_t* q_at(const GroupArgs& ga, int row, int j0, int hf) {
+  return ga.q + static_cast<int64_t>(row) * ga.ldq + static_cast<int64_t>(hf) * ga.nh + j0;
+}
+__device__ __forceinline__ uint8_t* qs_at(const GroupArgs& ga, int row, int j0, int hf) {
+  return ga.qs + (static_cast<int64_t>(hf) * ((ga.N + 31) / 32) + j0 / 32) * ga.lds + row;
+}
+__device__ __forceinline__ void q_store(const GroupArgs& ga, int row, int j0, int hf, const float (&v)[32]) {
+  QGroup g;
+  g.e = group_exponent(v);  // columns past N hold zeros
+  group_encode(v, g.e, g.q);
+  uint4* dst = reinterpret_cast<uint4*>(q_at(ga, row, j0, hf));
+  dst[0] = g.q[0];
+  if (j0 + 16 < ga.N) dst[1] = g.q[1];
+  *qs_at(ga, row, j0, hf) = static_cast<uint8_t>(g.e);
+}
+__device__ __forceinline__ QGroup q_load(const GroupArgs& ga, int row, int j0, int hf) {
+  QGroup g;
+  g.q[0] = g.q[1] = make_uint4(0, 0, 0, 0);
+  g.e = 1;
+  if (row < ga.M && j0 < ga.N) {
+    const uint4* src = reinterpret_cast<const uint4*>(q_at(ga, row, j0, hf));
+    g.q[0] = __ldg(src);
+    if (j0 + 16 < ga.N) g.q[1] = __ldg(src + 1);
+    g.e = __ldg(qs_at(ga, row, j0, hf));
+  }
+  return g;
+}
+// dH in v -> dZ in (v) or (dg, v = du), H in h.
+__device__ __forceinline__ void dgelu_q(const QGroup& z8, float (&v)[32], float (&h)[32]) {
+  group_decode(z8.q, z8.e, h);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] *= gelu_grad_f(h[i]);
+    h[i] = gelu_f(h[i]);
+  }
+}
+__device__ __forceinline__ void dswiglu_q(const QGroup& g8, const QGroup& u8, float (&dg)[32], float (&v)[32], float (&h)[32]) {
+  group_decode(g8.q, g8.e, dg);
+  group_decode(u8.q, u8.e, h);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    // one sigmoid per element: SiLU(g) = g s, SiLU'(g) = s (1 + g (1 - s))
+    const float g = dg[i], u = h[i], sg = sigmoid_fast(g), silu = g * sg;
+    dg[i] = v[i] * u * (sg * (1.0f + g * (1.0f - sg)));
+    v[i] *= silu;
+    h[i] = silu * u;
+  }
+}
+
 // Columns [half * BN/2, (half + 1) * BN/2) of the accumulator row this thread owns.
 __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t taddr, int row,
                               int n0, int half, bool narrow, int ks) {
@@ -241,6 +306,10 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
         if (ga.D) {
           store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, g);
           store_row_chunk_bf16(static_cast<__nv_bfloat16*>(ga.D) + ga.nh, ga.ldd, row, j0, ga.N, u);
+        }
+        if (ga.q) {
+          q_store(ga, row, j0, 0, g);
+          q_store(ga, row, j0, 1, u);
         }
         float h[32];
 #pragma unroll
@@ -304,6 +373,7 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
           for (int i = 0; i < 32; ++i) v[i] += b[i];
         }
         if (ga.D) store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, v);
+        if (ga.q) q_store(ga, row, j0, 0, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i]);
         store_row_chunk_bf16(ga.D2, ga.ldd2, row, j0, ga.N, v);
@@ -331,6 +401,21 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
         }
         store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, dg);
         store_row_chunk_bf16(static_cast<__nv_bfloat16*>(ga.D) + ga.nh, ga.ldd, row, j0, ga.N, v);
+        break;
+      }
+      case tpi::EPI_DGELU_Q: {
+        float h[32];
+        dgelu_q(q_load(ga, row, j0, 0), v, h);
+        store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, v);
+        if (ga.D2) store_row_chunk_bf16(ga.D2, ga.ldd2, row, j0, ga.N, h);
+        break;
+      }
+      case tpi::EPI_DSWIGLU_Q: {
+        float dg[32], h[32];
+        dswiglu_q(q_load(ga, row, j0, 0), q_load(ga, row, j0, 1), dg, v, h);
+        store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, dg);
+        store_row_chunk_bf16(static_cast<__nv_bfloat16*>(ga.D) + ga.nh, ga.ldd, row, j0, ga.N, v);
+        if (ga.D2) store_row_chunk_bf16(ga.D2, ga.ldd2, row, j0, ga.N, h);
         break;
       }
       default:
@@ -459,6 +544,10 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
       tmem_ld32(taddr + c * 32, g);
       tmem_ld32(taddr + 128 + c * 32, u);
       tc_wait_ld();
+      if (ga.q && row0 + lane < ga.M) {
+        q_store(ga, row0 + lane, j0, 0, g);
+        q_store(ga, row0 + lane, j0, 1, u);
+      }
       if (lane == 0) bulk_wait_read<0>();  // the last chunk's stores have read both tiles
       __syncwarp();
       if (ga.D) {
@@ -505,6 +594,7 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
     if (ga.D) stage_write(t0, lane, v);
+    if (ga.q && row0 + lane < ga.M) q_store(ga, row0 + lane, j0, 0, v);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i]);
     stage_write(t1, lane, v);
@@ -514,6 +604,71 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
       if (ga.D) tma_store_3d(&p.tmE[gi], t, j0, 0, row0);
       tma_store_3d(&p.tmX[gi], t + kEpiTile, j0, 0, row0);
       bulk_commit();
+    }
+  }
+}
+
+// Backward of an activation kept in 8 bits: dZ leaves through tmE, H through
+// tmX (when wanted). z0 / z1 hold the first chunk's groups, loaded while the
+// MMAs ran; each next chunk's are loaded before this one's are worked on.
+__device__ void epilogue_bwd_q_tma(const GemmParams& p, const GroupArgs& ga, int gi, uint32_t taddr, int row0, int n0,
+                                   int half, bool narrow, int lane, EpiStage& es, QGroup z0, QGroup z1) {
+  const bool sw = p.epi == tpi::EPI_DSWIGLU_Q;
+  uint8_t* t = es.buf;
+  const uint32_t t0 = smem_u32(t), t1 = t0 + kEpiTile;
+  const int cpw = narrow ? BN / 128 : BN / 64;  // 32-column chunks per warp half
+#pragma unroll 1
+  for (int c = half * cpw; c < (half + 1) * cpw; ++c) {
+    const int j0 = n0 + c * 32;
+    if (j0 >= ga.N) break;  // warp-uniform
+    float v[32];
+    tmem_ld32(taddr + c * 32, v);
+    const QGroup c0 = z0, c1 = z1;
+    if (c + 1 < (half + 1) * cpw) {
+      z0 = q_load(ga, row0 + lane, j0 + 32, 0);
+      if (sw) z1 = q_load(ga, row0 + lane, j0 + 32, 1);
+    }
+    tc_wait_ld();
+    float h[32];
+    if (sw) {
+      float dg[32];
+      dswiglu_q(c0, c1, dg, v, h);
+      if (lane == 0) bulk_wait_read<0>();  // the last chunk's stores have read both tiles
+      __syncwarp();
+      stage_write(t0, lane, dg);
+      stage_write(t1, lane, v);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmE[gi], t, j0, 0, row0);
+        bulk_commit();
+        tma_store_3d(&p.tmE[gi], t + kEpiTile, j0, 1, row0);
+        bulk_commit();
+        bulk_wait_read<1>();  // tile 0 has been read
+      }
+      __syncwarp();
+      if (ga.D2) {
+        stage_write(t0, lane, h);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&p.tmX[gi], t, j0, 0, row0);
+          bulk_commit();
+        }
+      }
+    } else {
+      dgelu_q(c0, v, h);
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      stage_write(t0, lane, v);
+      if (ga.D2) stage_write(t1, lane, h);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmE[gi], t, j0, 0, row0);
+        if (ga.D2) tma_store_3d(&p.tmX[gi], t + kEpiTile, j0, 0, row0);
+        bulk_commit();
+      }
     }
   }
 }
@@ -745,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const bool fwd = p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU;
       for (int g = 0; g < p.ngroups; ++g) {  // only the views the launch encoded
         if (!fwd || p.g[g].D) tma_prefetch_desc(&p.tmE[g]);
-        if (fwd || epi_inputs(p, p.g[g]) > 0) tma_prefetch_desc(&p.tmX[g]);
+        if (fwd || epi_inputs(p, p.g[g]) > 0 || p.g[g].D2) tma_prefetch_desc(&p.tmX[g]);
       }
     }
   }
@@ -985,6 +1140,13 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const bool pre = p.tma_epi && tma_rows && epi_inputs(p, ga) > 0 &&
                        n0 + half * (narrow ? BN / 4 : BN / 2) < ga.N;
       if (pre && lane == 0) epi_issue_inputs(p, gi, epi_inputs(p, ga), n0 + half * (narrow ? BN / 4 : BN / 2), trow, es);
+      QGroup z0{}, z1{};
+      const bool from_q = p.epi == tpi::EPI_DGELU_Q || p.epi == tpi::EPI_DSWIGLU_Q;
+      if (from_q && p.tma_epi) {  // and so do its 8-bit groups
+        const int j0 = n0 + half * (narrow ? BN / 4 : BN / 2);
+        z0 = q_load(ga, row0 + lane, j0, 0);
+        if (p.epi == tpi::EPI_DSWIGLU_Q) z1 = q_load(ga, row0 + lane, j0, 1);
+      }
       // warp-uniform: the epilogue's tcgen05.ld is warp-collective
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status))) {
         if (pre && lane == 0) {  // the prefetched copies land before the CTA may exit (bounded)
@@ -1000,6 +1162,8 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
         // past the last row of a scattered launch: nothing to store
       } else if (p.tma_epi && (p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU)) {
         epilogue_fwd_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
+      } else if (p.tma_epi && from_q) {
+        epilogue_bwd_q_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es, z0, z1);
       } else if (p.tma_epi) {
         ok = epilogue_tile_tma(p, ga, gi, taddr, trow, n0, half, narrow, pre, lane, es, abort_flag, p.status);
       } else if (p.plain_staged) {
@@ -1100,8 +1264,9 @@ bool tma_epilogue_ok(const GemmBatch& b, int nout, int ksplit) {
   }
   const bool fwd = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_BIAS_GELU;
   const bool bwd = b.epi == tpi::EPI_DGELU || b.epi == tpi::EPI_DSWIGLU;
-  if (!fwd && !bwd && b.epi != tpi::EPI_STORE) return false;
-  const bool halves = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_DSWIGLU;
+  const bool bwd_q = b.epi == tpi::EPI_DGELU_Q || b.epi == tpi::EPI_DSWIGLU_Q;
+  if (!fwd && !bwd && !bwd_q && b.epi != tpi::EPI_STORE) return false;
+  const bool halves = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_DSWIGLU || b.epi == tpi::EPI_DSWIGLU_Q;
   for (int i = 0; i < nout; ++i) {
     const GemmProblem& o = b.g[i];
     if (o.acc) return false;
@@ -1109,6 +1274,7 @@ bool tma_epilogue_ok(const GemmBatch& b, int nout, int ksplit) {
     if (!out || reinterpret_cast<uintptr_t>(out) % 16) return false;
     if (fwd && o.D && reinterpret_cast<uintptr_t>(o.D) % 16) return false;
     if (bwd && !o.aux) return false;
+    if (bwd_q && o.D2 && reinterpret_cast<uintptr_t>(o.D2) % 16) return false;
     if (!fwd && o.aux && reinterpret_cast<uintptr_t>(o.aux) % 16) return false;
     if (halves && (o.nh % 8 || o.N != o.nh)) return false;
   }
@@ -1317,6 +1483,15 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   if (b.kcat && b.epi != EPI_STORE)
     return fail(TP_ERR_ARG, "K-concatenated GEMM supports the plain epilogue only");
   const int nout = b.kcat ? 1 : b.n;
+  const bool from_q = b.epi == EPI_DGELU_Q || b.epi == EPI_DSWIGLU_Q;
+  for (int i = 0; i < nout; ++i) {
+    const GemmProblem& o = b.g[i];
+    const bool act = b.epi == EPI_BIAS_GELU || swiglu;
+    if (from_q && (!o.q || b.out_f32)) return fail(TP_ERR_ARG, "GEMM %d: no 8-bit pre-activation", i);
+    if (o.q && ((!from_q && !act) || !o.qs || !aligned16(o.q) || o.ldq % 16 || o.N % 16 ||
+                ((swiglu || b.epi == EPI_DSWIGLU_Q) && (o.nh % 16 || o.nh != o.N))))
+      return fail(TP_ERR_ALIGN, "GEMM %d: 8-bit pre-activations need rows of a multiple of 16 (N=%d)", i, o.N);
+  }
   for (int i = 0; i < nout; ++i)
     if (b.g[i].acc && (b.epi != EPI_STORE || b.ksplit > 1 || b.scatter_n || b.g[i].ldacc % 4 || !aligned16(b.g[i].acc)))
       return fail(TP_ERR_ARG, "GEMM %d: a running sum needs a plain dense output and 16-byte rows", i);
@@ -1367,6 +1542,10 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
       a.ldaux = o.ldaux;
       a.acc = o.acc;
       a.ldacc = o.ldacc;
+      a.q = o.q;
+      a.ldq = o.ldq;
+      a.qs = o.qs;
+      a.lds = o.lds;
       const int64_t t = static_cast<int64_t>((o.M + tile_m - 1) / tile_m) * a.tiles_n;
       if (tiles + t > 0x7fffffffLL) return fail(TP_ERR_UNSUPPORTED, "too many GEMM tiles");
       tiles += static_cast<int>(t);
@@ -1424,7 +1603,7 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
     }
   } else if (tma_epilogue_ok(b, nout, ksplit)) {
     p.tma_epi = 1;
-    const bool sw = b.epi == tpi::EPI_DSWIGLU || b.epi == tpi::EPI_SWIGLU;
+    const bool sw = b.epi == tpi::EPI_DSWIGLU || b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_DSWIGLU_Q;
     const bool fwd = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_BIAS_GELU;
     const uint64_t halves = sw ? 2 : 1;
     for (int i = 0; i < nout && p.tma_epi; ++i) {
@@ -1432,8 +1611,8 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
       bool good = true;
       // tmE: D (Z in the forward activations, where it may be absent)
       if (o.D) good = encode_epi(enc, &p.tmE[i], o.D, o.N, halves, sw ? o.nh : o.ldd, o.M, o.ldd) == TP_OK;
-      // tmX: H (forward activations) or the staged input
-      if (good && fwd) good = encode_epi(enc, &p.tmX[i], o.D2, o.N, 1, o.ldd2, o.M, o.ldd2) == TP_OK;
+      // tmX: H (the activations, computed forward or again) or the staged input
+      if (good && (fwd || o.D2)) good = encode_epi(enc, &p.tmX[i], o.D2, o.N, 1, o.ldd2, o.M, o.ldd2) == TP_OK;
       else if (good && o.aux)
         good = encode_epi(enc, &p.tmX[i], o.aux, o.N, halves, sw ? o.nh : o.ldaux, o.M, o.ldaux) == TP_OK;
       if (!good) p.tma_epi = 0;  // a view the encoder refuses: the direct epilogue serves

@@ -50,13 +50,15 @@ struct tp_plan {
   int group_wgrad;
   tpi::GemmBatch* wg_pend;  // NULL when nothing waits
   cudaStream_t wg_st;
-  // Scratch of the calls that may be captured into graphs (tpi::scratch):
-  // a block that a captured graph may hold is never freed before the plan.
+  // Scratch of the calls that refuse to grow it inside a capture (tpi::scratch).
   void* sc;
   size_t sc_bytes;
   int sc_device;
-  int sc_captured;
-  tpi::Retired* sc_retired;
+  // Whether a call of this plan was captured into a graph: workspace blocks
+  // replaced since then are kept until the plan is destroyed, since the graph
+  // replays with their addresses.
+  int captured;
+  tpi::Retired* retired;
 };
 
 namespace tpi {
@@ -105,6 +107,9 @@ tp_status persistent_grid(const void* kernel, int threads, int smem, int64_t uni
 
 // Device address of this device's status word (set by kernels on a timeout).
 tp_status device_status_word(unsigned** out);
+// Sets plan->captured when st is being captured (entry points that use the
+// plan's workspaces call it first).
+void note_capture(tp_plan* plan, cudaStream_t st);
 // Scratch of at least `bytes` on the current device, owned by the plan.
 tp_status workspace(tp_plan* plan, size_t bytes, void** out);
 // The plan's kPlanCounters arrival counters on the current device (zero at
@@ -119,8 +124,7 @@ tp_status workspace2(tp_plan* plan, size_t bytes, void** out);
 // Scratch of at least `bytes` on the current device for a call on `st`, owned
 // by the plan and shared by its calls in turn. Growing it allocates, so inside
 // a stream capture a call that needs more than the plan holds is refused
-// (TP_ERR_ARG); a block handed out inside a capture stays allocated until the
-// plan is destroyed, since the graph replays with its address.
+// (TP_ERR_ARG), and it sets plan->captured as note_capture does.
 tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out);
 
 // Validation helpers: each returns TP_OK or records an error.
@@ -224,6 +228,8 @@ enum Epi : int {
   EPI_SWIGLU = 2,      // gate/up pair: D (Z = [Zg|Zu]) optional, D2 (H) = SiLU(g) * u
   EPI_DGELU = 3,       // dH = acc; D (dZ) = dH * GELU'(aux Z)
   EPI_DSWIGLU = 4,     // dH = acc; aux = [Zg|Zu]; D (dZ) = [dH*u*SiLU'(g) | dH*SiLU(g)]
+  EPI_DGELU_Q = 5,     // as EPI_DGELU with Z from its 8-bit form; D2 (H, optional) = GELU(Z)
+  EPI_DSWIGLU_Q = 6,   // as EPI_DSWIGLU with Z from its 8-bit form; D2 (H, optional) = SiLU(g)*u
 };
 
 struct GemmProblem {
@@ -244,6 +250,14 @@ struct GemmProblem {
   // only; may be D itself when D is fp32.
   const float* acc;
   int64_t ldacc;
+  // Pre-activation in 8 bits (written beside EPI_BIAS_GELU / EPI_SWIGLU instead
+  // of Z, read by EPI_DGELU_Q / EPI_DSWIGLU_Q): e4m3 codes [M, N or 2 nh] with
+  // row stride ldq (a multiple of 16) and one biased power-of-two exponent per
+  // 32 columns of a row, group-major [groups, lds].
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* qs;
+  int64_t lds;
 };
 
 struct GemmBatch {

@@ -99,6 +99,8 @@ _SIGS = {
     "tp_vocab_cross_entropy": (_int, [_plan_p, _i64, _vpp, _vp, ctypes.c_float, _fp, _fp, _vpp, _vp]),
     "tp_vocab_linear_cross_entropy": (_int, [_plan_p, _i64, _vp, _vpp, _vp, ctypes.c_float, _fp, _fp, _vp, _vpp,
                                              _i64, _vp]),
+    "tp_column_fwd_ckpt8": (_int, [_plan_p, _i64, _vp, _vpp, _vpp, _vpp, _vpp, _vpp, _vp]),
+    "tp_row_bwd_ckpt8": (_int, [_plan_p, _i64, _vp, _vpp, _vpp, _vpp, _vpp, _vpp, _vpp, _fp, _vp]),
     "tp_gated_residual_norm_fwd": (_int, [_plan_p, _int, _i64, _vp, _vp, ctypes.c_float, _vp, _i64] + [_vp] * 7
                                    + [_vp]),
     "tp_gated_residual_norm_bwd": (_int, [_plan_p, _int, _i64, _vp, _vp, _fp, _vp, _vp, ctypes.c_float, _vp, _i64]
@@ -379,6 +381,29 @@ class Plan:
         check(lib.tp_column_fwd(self._h, WHICH[which], T, _ptr(X), _arr(W), _arr(bias), _arr(Z),
                                 _arr(H), _stream(stream)), "tp_column_fwd")
 
+    def ckpt8_shapes(self, T) -> tuple[tuple[int, int], tuple[int, int]]:
+        """Shapes of one shard's 8-bit pre-activation: codes (float8_e4m3fn or uint8) and scales (uint8)."""
+        k, n = self.ffn // self.p, 2 if self.act == "swiglu" else 1
+        return (T, n * k), (n * -(-k // 32), T)
+
+    def _check_ckpt8(self, T, Zq, Zs, W, W_shape, H):
+        codes, scales = self.ckpt8_shapes(T)
+        _want_shards("W", W, self.p, W_shape, self.torch_dtype)
+        _want_shards("Zq", Zq, self.p, codes, torch.float8_e4m3fn, torch.uint8)
+        _want_shards("Zs", Zs, self.p, scales, torch.uint8)
+        _want_shards("H", H, self.p, (T, self.ffn // self.p), self.torch_dtype)
+        return codes[1]
+
+    def column_fwd_ckpt8(self, T, X, W, bias, Zq, Zs, H, stream=None):
+        """tp_column_fwd_ckpt8: the MLP's column layer with Z kept as e4m3 codes Zq and scales Zs."""
+        n1 = self.ckpt8_shapes(T)[0][1]
+        self._check_ckpt8(T, Zq, Zs, W, (n1, self.hidden), H)
+        _want("X", X, (T, self.hidden), self.torch_dtype)
+        _want_shards("bias", bias, self.p, (n1,), self.torch_dtype)
+        with _device_of(X, W, bias, Zq, Zs, H):
+            check(lib.tp_column_fwd_ckpt8(self._h, T, _ptr(X), _arr(W), _arr(bias), _arr(Zq), _arr(Zs), _arr(H),
+                                          _stream(stream)), "tp_column_fwd_ckpt8")
+
     def row_fwd_partial(self, which, T, H, W, P, stream=None):
         check(lib.tp_row_fwd_partial(self._h, WHICH[which], T, _arr(H), _arr(W), _arr(P),
                                      _stream(stream)), "tp_row_fwd_partial")
@@ -468,6 +493,19 @@ class Plan:
     def row_bwd(self, which, T, dY, H, W, Z, dZ, dW=None, dbias=None, stream=None):
         check(lib.tp_row_bwd(self._h, WHICH[which], T, _ptr(dY), _arr(H), _arr(W), _arr(Z),
                              _arr(dZ), _arr(dW), _ptr(dbias), _stream(stream)), "tp_row_bwd")
+
+    def row_bwd_ckpt8(self, T, dY, W, Zq, Zs, H, dZ, dW=None, dbias=None, stream=None):
+        """tp_row_bwd_ckpt8: the MLP's row backward from Zq, Zs; H (optional without dW) receives the
+        recomputed activation."""
+        k = self.ffn // self.p
+        n1 = self._check_ckpt8(T, Zq, Zs, W, (self.hidden, k), H)
+        _want("dY", dY, (T, self.hidden), self.torch_dtype)
+        _want_shards("dZ", dZ, self.p, (T, n1), self.torch_dtype)
+        _want_shards("dW", dW, self.p, (self.hidden, k), self.torch_dtype)
+        _want("dbias", dbias, (self.hidden,), torch.float32)
+        with _device_of(dY, W, Zq, Zs, H, dZ, dW, dbias):
+            check(lib.tp_row_bwd_ckpt8(self._h, T, _ptr(dY), _arr(W), _arr(Zq), _arr(Zs), _arr(H), _arr(dZ), _arr(dW),
+                                       _ptr(dbias), _stream(stream)), "tp_row_bwd_ckpt8")
 
     def column_bwd(self, which, T, X, dZ, W, dW=None, dbias=None, dX_partials=None, stream=None):
         check(lib.tp_column_bwd(self._h, WHICH[which], T, _ptr(X), _arr(dZ), _arr(W), _arr(dW),

@@ -116,3 +116,46 @@ def test_gated_norm_binding_checks():
         call("layer", 8, x, x, x, stats=torch.zeros(2, 8))
     with pytest.raises(KeyError):
         call("batch", 8, x, x, x)
+
+
+def _cfwd(plan, T=4, X=A, W=A, bias=None, Zq=A, Zs=A + 1, H=A):
+    return tp.lib.tp_column_fwd_ckpt8(plan.handle, T, X, _arr(W), _arr(bias) if bias else None, _arr(Zq), _arr(Zs), _arr(H), None)
+
+
+def _rbwd(plan, T=4, dY=A, W=A, Zq=A, Zs=A + 1, H=A, dZ=A, dW=None, dbias=None):
+    return tp.lib.tp_row_bwd_ckpt8(plan.handle, T, dY, _arr(W), _arr(Zq), _arr(Zs), _arr(H) if H else None, _arr(dZ),
+                                   _arr(dW) if dW else None, dbias, None)
+
+
+def test_ckpt8_refusals():
+    gelu = tp.Plan(64, 64, 0, 1, "bf16", "gelu")
+    swiglu = tp.Plan(64, 64, 0, 1, "bf16", "swiglu")
+    assert _cfwd(tp.Plan(64, 64, 0, 1, "f32", "gelu")) == 4 and "bf16" in tp.last_error()
+    assert _cfwd(tp.Plan(64, 64, 0, 1, "bf16", "none")) == 1 and "activation" in tp.last_error()
+    assert _cfwd(tp.Plan(64, 0, 0, 1, "bf16", "gelu")) == 1 and "MLP" in tp.last_error()
+    assert _cfwd(tp.Plan(64, 72, 0, 1, "bf16", "gelu")) == 3 and "8-bit" in tp.last_error()
+    assert _cfwd(swiglu, bias=A) == 1 and "bias" in tp.last_error()
+    assert _cfwd(gelu, T=-1) == 1 and _cfwd(gelu, X=None) == 1 and _cfwd(gelu, W=None) == 1
+    assert _cfwd(gelu, Zq=A + 8) == 3 and _cfwd(gelu, Zs=None) == 1 and _cfwd(gelu, H=None) == 1
+    assert _cfwd(gelu, T=0, X=None, Zq=None, Zs=None, H=None) == 0
+    assert _rbwd(gelu, dY=None) == 1 and _rbwd(gelu, dZ=None) == 1 and _rbwd(gelu, Zs=None) == 1
+    assert _rbwd(gelu, H=None, dW=A) == 1 and "H" in tp.last_error()
+    assert _rbwd(gelu, dbias=A + 4) == 3
+    assert _rbwd(gelu, T=0, dY=None, Zq=None, Zs=None, dZ=None) == 0
+
+
+def test_ckpt8_shapes_and_binding_checks():
+    plan = tp.Plan(64, 2 * 1376, 0, 2, "bf16", "swiglu")
+    assert plan.ckpt8_shapes(5) == ((5, 2752), (86, 5))
+    assert tp.Plan(64, 80, 0, 1, "bf16", "gelu").ckpt8_shapes(7) == ((7, 80), (3, 7))
+    X = torch.zeros(5, 64).bfloat16()
+    W = [torch.zeros(2752, 64).bfloat16() for _ in range(2)]
+    H = [torch.zeros(5, 1376).bfloat16() for _ in range(2)]
+    q = [torch.zeros(5, 2752, dtype=torch.uint8) for _ in range(2)]
+    s = [torch.zeros(86, 5, dtype=torch.uint8) for _ in range(2)]
+    with pytest.raises(ValueError, match="Zs"):
+        plan.column_fwd_ckpt8(5, X, W, None, q, [x.T.contiguous() for x in s], H)
+    with pytest.raises(ValueError, match="Zq"):
+        plan.column_fwd_ckpt8(5, X, W, None, [x.float() for x in q], s, H)
+    with pytest.raises(ValueError, match="dZ"):
+        plan.row_bwd_ckpt8(5, X, [torch.zeros(64, 1376).bfloat16()] * 2, q, s, H, H)
