@@ -144,6 +144,11 @@ struct alignas(64) GemmParams {
   // Plain stores through the stage (plain_staged = 1): outputs that may be
   // another GPU's memory, EPI_STORE, bf16, no bias, residual or split.
   int plain_staged;
+  // EPI_CE (GemmBatch::ce_*): the vocab's size, labels, statistics.
+  int ce_vocab;
+  const int32_t* ce_labels;
+  float2* ce_stats;
+  int64_t ce_slots;
   CUtensorMap tmE[TP_MAX_SHARDS];
   CUtensorMap tmX[TP_MAX_SHARDS];
   unsigned* status;
@@ -177,6 +182,15 @@ __device__ __forceinline__ void kb_range(const GemmParams& p, const GroupArgs& g
     kb0 = 0;
     nkb = ga.num_kb;
   }
+}
+
+// K segments [lo, hi) of a tile: all of a K-concatenated output's, or its
+// split's equal share of them; one otherwise.
+__device__ __forceinline__ void seg_range(const GemmParams& p, int ks, int& lo, int& hi) {
+  const int n = p.kcat ? p.kcat : 1;
+  const int per = p.kcat && p.ksplit > 1 ? n / p.ksplit : n;
+  lo = p.kcat ? ks * per : 0;
+  hi = lo + per;
 }
 
 // A tile with at most BN / 2 valid columns left (the ragged last N tile of a
@@ -608,6 +622,87 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
   }
 }
 
+// Cross-entropy epilogue (EPI_CE): a thread has one row and a half tile's
+// columns (a slot). A first pass over the accumulator takes their largest score,
+// a second the exponentials relative to it: their sum, and, when gradients
+// follow, the exponentials themselves in bf16: one rounding (2^-8) beside the
+// gradient's own, with fp32's range, so that an entry far below its slot's
+// largest keeps its gradient (fp16 would be 2^-11 but lose what is below 2^-25).
+// The scores exist only here, in fp32. Padding columns and the row's label take
+// no part (the label's score is added in full precision later).
+__device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uint32_t taddr, int row0, int n0, int half,
+                            bool narrow, int lane, EpiStage& es) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int cpw = narrow ? BN / 128 : BN / 64;  // 32-column chunks per slot
+  const int row = row0 + lane, col0 = g * ga.N;
+  const bool row_ok = row < ga.M;
+  const int limit = min(ga.N, p.ce_vocab - col0);                 // columns from here on are padding
+  const int label = row_ok ? p.ce_labels[row] - col0 : -1;        // in this problem's columns
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = half * cpw; c < (half + 1) * cpw; ++c) {
+    const int j0 = n0 + c * 32;
+    if (j0 >= limit) break;  // warp-uniform
+    float v[32];
+    tmem_ld32(taddr + c * 32, v);
+    tc_wait_ld();
+    if (__any_sync(0xffffffffu, label >= j0 && label < j0 + 32) || j0 + 32 > limit) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) m = max3(m, v[i], v[i + 1]);
+  }
+  m *= kLog2e;
+  const float mo = m == -INFINITY ? 0.f : m;  // nothing left: every exp is 2^-inf = 0
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = half * cpw; c < (half + 1) * cpw; ++c) {
+    const int j0 = n0 + c * 32;
+    if (j0 >= ga.N) break;  // warp-uniform; padding columns are stored as zeros
+    float v[32];
+    tmem_ld32(taddr + c * 32, v);
+    tc_wait_ld();
+    if (__any_sync(0xffffffffu, label >= j0 && label < j0 + 32) || j0 + 32 > limit) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
+    }
+    uint32_t h[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float a = ex2(fmaf(v[i], kLog2e, -mo)), b = ex2(fmaf(v[i + 1], kLog2e, -mo));
+      sum += a + b;
+      h[i / 2] = pack_bf16x2(a, b);
+    }
+    if (!ga.D) continue;
+    if (p.tma_epi) {
+      uint8_t* t = es.buf + es.slot * kEpiTile;
+      if (lane == 0) bulk_wait_read<1>();  // the store issued from this tile two chunks ago has read it
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        st_shared_v4(sw64(smem_u32(t), lane, q), make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmE[g], t, j0, 0, row0);
+        bulk_commit();
+      }
+      es.slot ^= 1;
+    } else if (row_ok) {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(ga.D) + static_cast<int64_t>(row) * ga.ldd + j0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j0 + q * 8 < ga.N)
+          *reinterpret_cast<uint4*>(dst + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+    }
+  }
+  if (row_ok)
+    p.ce_stats[row * p.ce_slots + 2 * (static_cast<int64_t>(g) * ga.tiles_n + n0 / p.tile_n) + half] = make_float2(m, sum);
+}
+
 // Backward of an activation kept in 8 bits: dZ leaves through tmE, H through
 // tmX (when wanted). z0 / z1 hold the first chunk's groups, loaded while the
 // MMAs ran; each next chunk's are loaded before this one's are worked on.
@@ -899,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     } else if (p.tma_epi) {
       const bool fwd = p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU;
       for (int g = 0; g < p.ngroups; ++g) {  // only the views the launch encoded
-        if (!fwd || p.g[g].D) tma_prefetch_desc(&p.tmE[g]);
+        if (p.g[g].D) tma_prefetch_desc(&p.tmE[g]);
         if (fwd || epi_inputs(p, p.g[g]) > 0 || p.g[g].D2) tma_prefetch_desc(&p.tmX[g]);
       }
     }
@@ -974,8 +1069,9 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const bool half_b = p.narrow_all || (p.b_mn && narrow_tile(p, ga, n0));
       const uint32_t b_bytes = half_b ? C::B_BYTES / 2 : C::B_BYTES;
       const int b_blocks = (half_b ? C::B_ROWS / 2 : C::B_ROWS) / 64;  // MN-major 64-column blocks
-      const int nseg = p.kcat ? p.kcat : 1;
-      for (int sg = 0; sg < nseg && ok; ++sg) {
+      int seg_lo, seg_hi;
+      seg_range(p, ks, seg_lo, seg_hi);
+      for (int sg = seg_lo; sg < seg_hi && ok; ++sg) {
         const int gi = p.kcat ? sg : g;  // tensor maps of this K segment
         const int nkb = p.kcat ? p.seg_kb[sg] : kb_count;
         for (int kb = 0; kb < nkb; ++kb) {
@@ -1065,7 +1161,9 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       kb_range(p, p.g[g], ks, kb_first, num_kb);
       if (p.kcat) {
         num_kb = 0;
-        for (int sg = 0; sg < p.kcat; ++sg) num_kb += p.seg_kb[sg];
+        int seg_lo, seg_hi;
+        seg_range(p, ks, seg_lo, seg_hi);
+        for (int sg = seg_lo; sg < seg_hi; ++sg) num_kb += p.seg_kb[sg];
       }
       if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
       tc_fence_after();
@@ -1160,6 +1258,8 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
                              static_cast<uint32_t>(acc * BN);
       if (p.tma_epi && !tma_rows) {
         // past the last row of a scattered launch: nothing to store
+      } else if (p.epi == tpi::EPI_CE) {
+        epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, es);
       } else if (p.tma_epi && (p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU)) {
         epilogue_fwd_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi && from_q) {
@@ -1265,13 +1365,13 @@ bool tma_epilogue_ok(const GemmBatch& b, int nout, int ksplit) {
   const bool fwd = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_BIAS_GELU;
   const bool bwd = b.epi == tpi::EPI_DGELU || b.epi == tpi::EPI_DSWIGLU;
   const bool bwd_q = b.epi == tpi::EPI_DGELU_Q || b.epi == tpi::EPI_DSWIGLU_Q;
-  if (!fwd && !bwd && !bwd_q && b.epi != tpi::EPI_STORE) return false;
+  if (!fwd && !bwd && !bwd_q && b.epi != tpi::EPI_STORE && b.epi != tpi::EPI_CE) return false;
   const bool halves = b.epi == tpi::EPI_SWIGLU || b.epi == tpi::EPI_DSWIGLU || b.epi == tpi::EPI_DSWIGLU_Q;
   for (int i = 0; i < nout; ++i) {
     const GemmProblem& o = b.g[i];
     if (o.acc) return false;
     const void* out = fwd ? o.D2 : o.D;  // the output every tile writes
-    if (!out || reinterpret_cast<uintptr_t>(out) % 16) return false;
+    if ((!out && b.epi != tpi::EPI_CE) || reinterpret_cast<uintptr_t>(out) % 16) return false;
     if (fwd && o.D && reinterpret_cast<uintptr_t>(o.D) % 16) return false;
     if (bwd && !o.aux) return false;
     if (bwd_q && o.D2 && reinterpret_cast<uintptr_t>(o.D2) % 16) return false;
@@ -1501,8 +1601,10 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   const int sms = device_sms();
   int ksplit = b.ksplit > 1 ? b.ksplit : 1;
   if (ksplit > 1) {
-    if (b.kcat || b.scatter_n || b.epi != EPI_STORE || !b.out_f32)
-      return fail(TP_ERR_ARG, "split K needs plain fp32 outputs (no K concatenation or scatter)");
+    if (b.scatter_n || b.epi != EPI_STORE || !b.out_f32)
+      return fail(TP_ERR_ARG, "split K needs plain fp32 outputs (no scatter)");
+    if (b.kcat && b.n % ksplit)
+      return fail(TP_ERR_ARG, "split K of a K concatenation takes whole segments: %d over %d", ksplit, b.n);
     for (int i = 1; i < b.n; ++i)
       if (b.g[i].K != b.g[0].K) return fail(TP_ERR_ARG, "split K needs every problem with the same K");
   }
@@ -1574,7 +1676,7 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   if (ksplit > 1) {
     const int nkb = (b.g[0].K + BK - 1) / BK;
     const int kbps = (nkb + ksplit - 1) / ksplit;
-    if ((nkb + kbps - 1) / kbps != ksplit)
+    if (!b.kcat && (nkb + kbps - 1) / kbps != ksplit)
       return fail(TP_ERR_ARG, "split K of %d over %d K blocks leaves a split empty", ksplit, nkb);
     if (static_cast<int64_t>(tiles) * ksplit > 0x7fffffffLL) return fail(TP_ERR_UNSUPPORTED, "too many GEMM tiles");
     p.ksplit = ksplit;
@@ -1626,6 +1728,17 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   p.b_mn = b.b_mn;
   p.epi = b.epi;
   p.out_f32 = b.out_f32;
+  if (b.epi == EPI_CE) {
+    for (int i = 1; i < b.n; ++i)
+      if (b.g[i].N != b.g[0].N) return fail(TP_ERR_ARG, "cross-entropy GEMM: problem %d has another width", i);
+    if (b.kcat || b.scatter_n || ksplit > 1 || !b.ce_labels || !b.ce_stats ||
+        b.ce_slots < 2 * static_cast<int64_t>(b.n) * p.g[0].tiles_n)
+      return fail(TP_ERR_ARG, "cross-entropy GEMM: statistics of %lld slots", static_cast<long long>(b.ce_slots));
+    p.ce_vocab = b.ce_vocab;
+    p.ce_labels = b.ce_labels;
+    p.ce_stats = b.ce_stats;
+    p.ce_slots = b.ce_slots;
+  }
   s = device_status_word(&p.status);
   if (s != TP_OK) return s;
   p.dyn_sched = dynamic_schedule(tiles, sms / pair) ? 1 : 0;
@@ -1635,6 +1748,10 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   }
   if (pair == 2) return launch_kernel<2>(p, tiles, sms, st);
   return launch_kernel<1>(p, tiles, sms, st);
+}
+
+int gemm_tile_cols(const GemmBatch& b) {
+  return b.epi == EPI_SWIGLU || choose_layout(b, device_sms()).narrow ? BN / 2 : BN;
 }
 
 bool gemm_fills_gpu(const GemmBatch& b) {
@@ -1705,60 +1822,68 @@ tp_status launch_gemm_split(GemmBatch w, int s, float* part, cudaStream_t st) {
                        TP_BF16, st);
 }
 
-int gemm_cat_split(const GemmBatch& b) {
-  if (!b.kcat || b.scatter_n || b.epi != EPI_STORE || b.n < 1) return 0;
-  for (int i = 0; i < b.n; ++i)
-    if (b.g[i].K != b.g[0].K || b.g[i].bias || b.g[i].aux || b.g[i].acc) return 0;
-  const int sms = device_sms();
-  const int nkb = (b.g[0].K + BK - 1) / BK;
-  double best_cost = 0.0;
-  choose_layout(b, sms, &best_cost);
-  int best = 0;
+namespace {
+// The batch that computes b's output as `parts` partial sums: whole segments
+// together up to one per segment, else every segment split.
+GemmBatch cat_parts(const GemmBatch& b, int parts) {
   GemmBatch t = b;
-  t.kcat = false;
   t.out_f32 = true;
+  if (parts < b.n) {
+    t.ksplit = parts;
+    return t;
+  }
+  t.kcat = false;
+  t.ksplit = parts / b.n;
   for (int i = 1; i < b.n; ++i) {
     t.g[i].M = b.g[0].M;
     t.g[i].N = b.g[0].N;
   }
+  return t;
+}
+}  // namespace
+
+int gemm_cat_split(const GemmBatch& b) {
+  if (!b.kcat || b.scatter_n || b.epi != EPI_STORE || b.n < 1) return 1;
+  for (int i = 0; i < b.n; ++i)
+    if (b.g[i].K != b.g[0].K || b.g[i].bias || b.g[i].aux || b.g[i].acc) return 1;
+  const int sms = device_sms();
+  const int nkb = (b.g[0].K + BK - 1) / BK;
   const double out = static_cast<double>(b.g[0].M) * b.g[0].N;
-  for (int s = 1; s * b.n <= TP_MAX_SHARDS; ++s) {
-    if (s * b.n == 1) continue;
-    if (s > 1 && nkb < 4 * s) break;
-    const int kbps = (nkb + s - 1) / s;
-    if ((nkb + kbps - 1) / kbps != s) continue;  // a split would be empty
-    t.ksplit = s;
+  double best_cost = 0.0;
+  choose_layout(b, sms, &best_cost);
+  int best = 1;
+  for (int parts = 2; parts <= TP_MAX_SHARDS; ++parts) {
+    if (parts < b.n ? b.n % parts : parts % b.n) continue;
+    if (parts > b.n) {
+      const int s = parts / b.n, kbps = (nkb + s - 1) / s;
+      if (nkb < 4 * s || (nkb + kbps - 1) / kbps != s) continue;  // short or empty splits
+    }
     double c = 0.0;
-    choose_layout(t, sms, &c);
-    c += out * (4.0 * s * b.n + 2.0) / 6000.0 + 1600.0;  // the partials' reduce, as in gemm_split_k
-    if (c < 0.9 * best_cost) {
+    choose_layout(cat_parts(b, parts), sms, &c);
+    c += out * (4.0 * parts + 2.0) / 6000.0 + 1600.0;  // the partials' reduce, as in gemm_split_k
+    if (c < 0.97 * best_cost) {
       best_cost = c;
-      best = s;
+      best = parts;
     }
   }
   return best;
 }
 
-tp_status launch_gemm_cat_split(GemmBatch b, int s, float* part, cudaStream_t st) {
-  const int n = b.n;
+tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cudaStream_t st) {
   const int64_t M = b.g[0].M, N = b.g[0].N, mn = M * N;
   MutPtrArray out{};
   out.p[0] = b.g[0].D;
-  for (int i = 0; i < n; ++i) {
-    b.g[i].M = static_cast<int>(M);
-    b.g[i].N = static_cast<int>(N);
-    b.g[i].D = part + i * mn;
-    b.g[i].ldd = N;
+  GemmBatch t = cat_parts(b, parts);
+  for (int i = 0; i < b.n; ++i) {
+    t.g[i].D = part + (t.kcat ? 0 : i * mn);
+    t.g[i].ldd = N;
   }
-  b.kcat = false;
-  b.out_f32 = true;
-  b.ksplit = s;
-  b.split_stride = n * mn;
-  tp_status r = launch_gemm_bf16(b, st);
+  t.split_stride = t.kcat ? mn : b.n * mn;
+  tp_status r = launch_gemm_bf16(t, st);
   if (r != TP_OK) return r;
   PtrArray P{};
-  for (int j = 0; j < s * n; ++j) P.p[j] = part + j * mn;
-  return launch_reduce(P, s * n, nullptr, nullptr, PtrArray{}, false, out, false, 1, M, N, TP_F32, TP_BF16, st);
+  for (int j = 0; j < parts; ++j) P.p[j] = part + j * mn;
+  return launch_reduce(P, parts, nullptr, nullptr, PtrArray{}, false, out, false, 1, M, N, TP_F32, TP_BF16, st);
 }
 
 }  // namespace tpi

@@ -230,6 +230,7 @@ enum Epi : int {
   EPI_DSWIGLU = 4,     // dH = acc; aux = [Zg|Zu]; D (dZ) = [dH*u*SiLU'(g) | dH*SiLU(g)]
   EPI_DGELU_Q = 5,     // as EPI_DGELU with Z from its 8-bit form; D2 (H, optional) = GELU(Z)
   EPI_DSWIGLU_Q = 6,   // as EPI_DSWIGLU with Z from its 8-bit form; D2 (H, optional) = SiLU(g)*u
+  EPI_CE = 7,          // scores of the vocab: per row and slot of columns max and sum of exp; D (optional) = exps
 };
 
 struct GemmProblem {
@@ -281,6 +282,16 @@ struct GemmBatch {
   // Outputs that may be another GPU's memory (a peer group's receive
   // buffers): the epilogue writes them with plain stores, never TMA.
   bool plain_stores;
+  // EPI_CE: problem i's columns are vocab entries [i * N, (i + 1) * N), those
+  // from ce_vocab on padding. Each half of a tile's columns is a slot: for row r
+  // it writes ce_stats[r * ce_slots + slot] = (m, s), m the largest score times
+  // log2 e and s the sum of 2^(score log2 e - m) over its columns except padding
+  // and the row's label (both count as exp 0; m = -inf if none is left), and D
+  // (optional) those exps in bf16.
+  int ce_vocab;
+  const int32_t* ce_labels;
+  float2* ce_stats;
+  int64_t ce_slots;
   // Split K (bf16 path, EPI_STORE, fp32 outputs, every problem with the same
   // K): ksplit > 1 runs each output tile ksplit times over consecutive K
   // ranges, split s writing its fp32 partial at g[i].D + s * split_stride.
@@ -290,6 +301,10 @@ struct GemmBatch {
 
 // bf16 tcgen05 tensor-core path (tp_gemm_sm100.cu).
 tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st);
+// Output columns per tile that a bf16 launch of b will use (256 or 128). Its
+// slots (EPI_CE): two per tile, each half of the columns the tile multiplies,
+// which are 256, or 128 where the launch or the tile (at most 128 left) is narrow.
+int gemm_tile_cols(const GemmBatch& b);
 // Whether a bf16 launch of b has at least as many tiles as CTA units (pairs or
 // CTAs) on this device, i.e. leaves no SM idle in its first wave.
 bool gemm_fills_gpu(const GemmBatch& b);
@@ -301,11 +316,12 @@ int gemm_split_k(const GemmBatch& b);
 // adds them in order into D[i].
 tp_status launch_gemm_split(GemmBatch b, int s, float* part, cudaStream_t st);
 // The K-concatenated batch b (one bf16 output, D dense [M, N], equal segments) as
-// n * s separate partial products (n * s <= 16) and one ordered reduce, or as
-// it is: the s that takes least time by the estimate, 0 for the latter. Few
-// output tiles with a long K gain from it.
+// `parts` fp32 partial sums (<= 16 of M * N floats in `part`: whole segments
+// together, or every segment split) and one ordered reduce. gemm_cat_split: the
+// parts that take least time by the estimate, 1 for b as it is; a last wave of
+// tiles that fills few SMs, or few tiles with a long K, gain from it.
 int gemm_cat_split(const GemmBatch& b);
-tp_status launch_gemm_cat_split(GemmBatch b, int s, float* part, cudaStream_t st);
+tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cudaStream_t st);
 // fp32 FMA path (tp_gemm_simt.cu): the same epilogues, grouping and K concatenation.
 tp_status launch_gemm_f32(const GemmBatch& b, cudaStream_t st);
 

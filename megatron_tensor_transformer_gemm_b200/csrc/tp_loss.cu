@@ -5,7 +5,16 @@
 //   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label
 //   d_tv  = (exp(z_tv - lse_t) - [v = label]) * scale,  dX = d W,  dW = d^T X
 //
-// Tokens are taken a chunk at a time; the workspace holds one chunk's scores.
+// Tokens are taken a chunk at a time. For bf16 plans the scores live only in the
+// tensor cores' fp32 accumulators: the GEMM's epilogue leaves, per row and slot of
+// 64 or 128 columns, their maximum m and sum of 2^(z log2 e - m), and, when
+// gradients are wanted, the exponentials themselves in bf16 (relative to the slot's
+// maximum). A row kernel merges the slots (the running maximum and sum of a
+// softmax, joined), adds the label's score, and turns the exponentials into d in
+// place with one factor 2^(m - lse2) * scale per slot; then the two products. So
+// each score is computed once: 6 T V h operations for loss and gradients, against
+// 8 for recomputing the scores in the backward, at 6 bytes of traffic per score.
+// fp32 plans keep the chunk's scores in fp32.
 #include <algorithm>
 
 #include "tp_device.cuh"
@@ -46,9 +55,8 @@ __device__ __forceinline__ float2 block_merge(float2 v, float2* red) {
 // One CTA per token row of fp32 scores z [rows, ld]: a pass for the running
 // (max, sum), then (d != NULL) a pass that writes d, which may be z itself.
 constexpr int kRowThreads = 512;
-template <typename Out>
 __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, int64_t ld, int vocab, const int32_t* labels,
-                                                              float scale, float* loss, float* lse_out, Out* d,
+                                                              float scale, float* loss, float* lse_out, float* d,
                                                               unsigned* status) {
   tpd::pdl_entry();
   __shared__ float2 red[kRowThreads / 32];
@@ -78,7 +86,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
   }
   if (!d) return;
   __syncthreads();  // the label's score has been read: d may be z
-  Out* drow = d + t * ld;
+  float* drow = d + t * ld;
   for (int64_t c = threadIdx.x * 4; c < ld; c += kRowThreads * 4) {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (!ignore && c < vocab) {
@@ -90,10 +98,99 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
         x[e] = (pr - (c + e == label ? 1.f : 0.f)) * scale;
       }
     }
-    if constexpr (sizeof(Out) == 2)
-      *reinterpret_cast<uint2*>(drow + c) = make_uint2(tpd::pack_bf16x2(x[0], x[1]), tpd::pack_bf16x2(x[2], x[3]));
-    else
-      *reinterpret_cast<float4*>(drow + c) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(drow + c) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// Where a shard's column lies in the statistics: see gemm_tile_cols.
+__device__ __forceinline__ int slot_of(int col, int Vs, int tile_cols) {
+  const int tile = col / tile_cols, n0 = tile * tile_cols;
+  return 2 * tile + (col - n0) / (Vs - n0 <= 128 || tile_cols == 128 ? 64 : 128);
+}
+
+// Merges a row's slot statistics, adds the label's score and writes loss and
+// lse; then (e != NULL) turns the row's exponentials into d in place.
+// The label's score is a dot product of its own, in fp32 by the CTA: the tensor
+// cores' long accumulation is less exact, and a confident token's loss is the
+// difference of lse and this score. gridDim.y CTAs share a row's second part
+// (few rows: the merge is short and repeated by each).
+constexpr int kFinThreads = 256;
+__global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
+    const float2* stats, int slots, int tile_cols, int shard_slots, const __nv_bfloat16* X,
+    const __grid_constant__ PtrArray W, int h, int vocab, int Vs, int p, const int32_t* labels, float scale, float* loss,
+    float* lse_out, uint4* e, unsigned* status) {
+  tpd::pdl_entry();
+  __shared__ float2 red[kFinThreads / 32];
+  __shared__ float dot[kFinThreads / 32];
+  const int64_t t = blockIdx.x;
+  const int label = labels[t];
+  const bool ignore = label < 0 || label >= vocab;
+  float z = 0.f;
+  if (!ignore) {
+    const uint4* x = reinterpret_cast<const uint4*>(X + t * h);
+    const int sh = label / Vs;
+    const uint4* w = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(W.p[sh]) +
+                                                    static_cast<int64_t>(label - sh * Vs) * h);
+    for (int i = threadIdx.x; i < h / 8; i += kFinThreads) {
+      const uint4 a = x[i], b = w[i];
+      const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = tpd::unpack_bf16x2(au[q]), g = tpd::unpack_bf16x2(bu[q]);
+        z = fmaf(f.x, g.x, z);
+        z = fmaf(f.y, g.y, z);
+      }
+    }
+  }
+  const float2* st = stats + t * slots;
+  float2 acc = make_float2(-INFINITY, 0.f);
+  for (int i = threadIdx.x; i < slots; i += kFinThreads) acc = merge(acc, st[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  if ((threadIdx.x & 31) == 0) dot[threadIdx.x >> 5] = z;
+  float2 tot = block_merge<kFinThreads>(acc, red);  // its barrier covers dot
+  z = 0.f;
+#pragma unroll
+  for (int w = 0; w < kFinThreads / 32; ++w) z += dot[w];
+  const float z2 = z * kLog2e;
+  if (!ignore) tot = merge(tot, make_float2(z2, 1.f));
+  const float lse2 = tot.x + log2f(tot.y);
+  if (threadIdx.x == 0 && blockIdx.y == 0) {
+    if (label >= vocab) atomicOr(status, kStatusBadIndex);
+    loss[t] = ignore ? 0.f : (tot.x - z2 + log2f(tot.y)) * kLn2;
+    if (lse_out) lse_out[t] = lse2 * kLn2;
+  }
+  if (!e) return;
+  const int nv = Vs / 8, total = p * nv;  // 16-byte vectors of the row
+  uint4* row = e + t * total;
+  const int per = (total + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+  const int lo = static_cast<int>(blockIdx.y) * per, hi = min(total, lo + per);
+  if (ignore) {
+    for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) row[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float at_label = (tpd::ex2(z2 - lse2) - 1.f) * scale;
+#pragma unroll 4
+  for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) {
+    const uint4 u = row[i];
+    const int sh = i / nv, c = (i - sh * nv) * 8;
+    const float m = st[sh * shard_slots + slot_of(c, Vs, tile_cols)].x;  // -inf: all its exps are 0
+    const float f = tpd::ex2(m - lse2) * scale;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float d[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 v = tpd::unpack_bf16x2(w[q]);
+      d[2 * q] = v.x * f;
+      d[2 * q + 1] = v.y * f;
+    }
+    if (i == label / 8) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q == label % 8) d[q] = at_label;
+    }
+    row[i] = make_uint4(tpd::pack_bf16x2(d[0], d[1]), tpd::pack_bf16x2(d[2], d[3]), tpd::pack_bf16x2(d[4], d[5]),
+                        tpd::pack_bf16x2(d[6], d[7]));
   }
 }
 
@@ -101,12 +198,12 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Tokens per chunk: the caller's, or one chunk for all tokens unless chunks of
 // about 1 GiB of scores make the workspace (scores and fp32 sums of dW) smaller.
-int64_t pick_chunk(int64_t T, int64_t Vp, int64_t h, size_t score_bytes, bool dw_sums, int64_t asked) {
+int64_t pick_chunk(int64_t T, int64_t Vp, int64_t h, double score_bytes, bool dw_sums, int64_t asked) {
   if (asked > 0) return std::min(asked, T);
   const double all = static_cast<double>(T) * Vp * score_bytes;
   const double part = static_cast<double>(1u << 30);
   if (all <= part + (dw_sums ? 4.0 * Vp * h : 0.0)) return T;
-  const int64_t most = std::max<int64_t>(1024, static_cast<int64_t>(part / (static_cast<double>(Vp) * score_bytes)) / 256 * 256);
+  const int64_t most = std::max<int64_t>(1024, static_cast<int64_t>(part / (Vp * score_bytes)) / 256 * 256);
   const int64_t n = (T + most - 1) / most;
   return std::min(T, ((T + n - 1) / n + 255) / 256 * 256);
 }
@@ -122,7 +219,8 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
   const int p = plan->p, h = plan->hidden, V = plan->vocab, Vp = plan->vocab_padded, Vs = Vp / p;
   const size_t es = dsize(plan->dtype);
   const bool grad = dX || dW.p[0], dw = dW.p[0] != nullptr;
-  const int64_t Tc = pick_chunk(T, Vp, h, bf ? 6 : 4, bf && dw, chunk);
+  // without gradients a bf16 plan keeps 8 bytes per slot of at least 64 scores
+  const int64_t Tc = pick_chunk(T, Vp, h, !bf || grad ? static_cast<double>(es) : 0.125, bf && dw, chunk);
   const int64_t nch = (T + Tc - 1) / Tc;
   unsigned* status = nullptr;
   TP_TRY(device_status_word(&status));
@@ -170,26 +268,12 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     return b;
   };
 
-  // scratch: fp32 scores | d | fp32 sums of dW | split-K partials
-  const int sx = bf && dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 0;
-  const int sw = bf && dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
-  const size_t z_bytes = round256(static_cast<size_t>(Tc) * Vp * 4);
-  const size_t d_bytes = bf && grad ? round256(static_cast<size_t>(Tc) * Vp * 2) : 0;
-  const size_t acc_bytes = bf && dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
-  const size_t part_bytes = std::max(static_cast<size_t>(sx) * p * Tc * h * 4, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
-  void* ws = nullptr;
-  TP_TRY(scratch(plan, z_bytes + d_bytes + acc_bytes + part_bytes, st, &ws));
-  float* z = static_cast<float*>(ws);
-  uint8_t* db = static_cast<uint8_t*>(ws) + (bf ? z_bytes : 0);
-  float* acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + z_bytes + d_bytes);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + z_bytes + d_bytes + acc_bytes);
-
-  for (int64_t c = 0; c < nch; ++c) {
-    const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
+  // the scores of a chunk: fp32 plans store them, bf16 plans their statistics
+  auto score_batch = [&](void* out, int64_t t0, int64_t n) {
     GemmBatch b{};
     b.n = p;
-    b.epi = EPI_STORE;
-    b.out_f32 = true;
+    b.epi = bf ? EPI_CE : EPI_STORE;
+    b.out_f32 = !bf;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
       g.M = static_cast<int>(n);
@@ -199,24 +283,56 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
       g.lda = h;
       g.B = W.p[i];
       g.ldb = h;
-      g.D = z + static_cast<size_t>(i) * Vs;
+      g.D = out ? static_cast<uint8_t*>(out) + static_cast<size_t>(i) * Vs * es : nullptr;
       g.ldd = Vp;
     }
-    TP_TRY(bf ? launch_gemm_bf16(b, st) : launch_gemm_f32(b, st));
-    if (bf)
-      (void)launch(ce_rows_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st, z,
-                   static_cast<int64_t>(Vp), V, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
-                   grad ? reinterpret_cast<__nv_bfloat16*>(db) : nullptr, status);
-    else
-      (void)launch(ce_rows_kernel<float>, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st, z,
-                   static_cast<int64_t>(Vp), V, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
-                   grad ? reinterpret_cast<float*>(db) : nullptr, status);
+    b.ce_vocab = V;
+    b.ce_labels = labels + t0;
+    return b;
+  };
+  // slots of a row at most (narrow tiles of 128 columns have two of 64)
+  const int64_t max_slots = bf ? 2LL * p * ((Vs + 127) / 128) : 0;
+
+  // scratch: d (from the exponentials or scores) | statistics | fp32 sums of dW | split-K partials
+  const int sx = bf && dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 1;
+  const int sw = bf && dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
+  const size_t d_bytes = !bf || grad ? round256(static_cast<size_t>(Tc) * Vp * es) : 0;
+  const size_t st_bytes = round256(static_cast<size_t>(Tc) * max_slots * sizeof(float2));
+  const size_t acc_bytes = bf && dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
+  const size_t part_bytes = std::max(sx > 1 ? static_cast<size_t>(sx) * Tc * h * 4 : 0, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
+  void* ws = nullptr;
+  TP_TRY(scratch(plan, d_bytes + st_bytes + acc_bytes + part_bytes, st, &ws));
+  uint8_t* db = static_cast<uint8_t*>(ws);
+  float2* stats = reinterpret_cast<float2*>(db + d_bytes);
+  float* acc = reinterpret_cast<float*>(db + d_bytes + st_bytes);
+  float* part = reinterpret_cast<float*>(db + d_bytes + st_bytes + acc_bytes);
+
+  for (int64_t c = 0; c < nch; ++c) {
+    const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
+    GemmBatch b = score_batch(!bf || grad ? db : nullptr, t0, n);
+    if (bf) {
+      const int tile = gemm_tile_cols(b);
+      const int shard_slots = 2 * ((Vs + tile - 1) / tile);
+      b.ce_stats = stats;
+      b.ce_slots = static_cast<int64_t>(p) * shard_slots;
+      TP_TRY(launch_gemm_bf16(b, st));
+      // a few rows: enough CTAs a row to fill the GPU with the second part
+      const int64_t parts = grad ? std::max<int64_t>(1, std::min<int64_t>(512 / n, Vp / 8 / kFinThreads)) : 1;
+      (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
+                   stats, static_cast<int>(b.ce_slots), tile, shard_slots,
+                   static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h, V, Vs, p, labels + t0, scale, loss + t0,
+                   lse ? lse + t0 : nullptr, grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
+    } else {
+      TP_TRY(launch_gemm_f32(b, st));
+      (void)launch(ce_rows_kernel, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st,
+                   reinterpret_cast<const float*>(db), static_cast<int64_t>(Vp), V, labels + t0, scale, loss + t0,
+                   lse ? lse + t0 : nullptr, grad ? reinterpret_cast<float*>(db) : nullptr, status);
+    }
     TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
     if (dX) {
       const GemmBatch x = dx_batch(db, t0, n);
-      const int s = bf ? (n == Tc ? sx : 0) : 0;
       if (!bf) TP_TRY(launch_gemm_f32(x, st));
-      else if (s > 0) TP_TRY(launch_gemm_cat_split(x, s, part, st));
+      else if (sx > 1) TP_TRY(launch_gemm_cat_split(x, sx, part, st));
       else TP_TRY(launch_gemm_bf16(x, st));
     }
     if (dw) {
