@@ -1,0 +1,203 @@
+// fp32 GEMM on the FMA units over matrices whose rows are spread over the shards:
+// D[M, N] = A[M, K] . B[N, K]^T (+ D), every product and sum in fp32. The shards of
+// a vocab-sharded weight are blocks of rows of one [Vp, hidden] matrix, so one
+// launch covers all of them whichever dimension the vocab is: N (scores), K (the
+// input gradient) or M (the weight gradient).
+//
+// A CTA of 256 threads computes a (16 TM) x 128 tile, a thread TM x 8 of it in
+// registers, over K blocks of 16 that two shared-memory buffers hold in [K][M] and
+// [K][N] order: the next block's global loads are in flight while this one is
+// multiplied. It is bound by the FMA units (128 a clock and SM, 72 TFLOP/s at the
+// clocks seen). TM = 8 does the work of a block in 32 fused multiply-adds per
+// 16-byte shared load; TM = 2 is for few rows, where the tile's height is what is
+// wasted. Launches with few tiles split K: split s writes its own partial of D and
+// an ordered reduce adds them (which also shortens the running sums).
+#include <algorithm>
+
+#include "tp_device.cuh"
+#include "tp_internal.h"
+
+namespace {
+
+using tpi::FmaGemm;
+using tpi::RowBlocks;
+
+constexpr int kBN = 128;
+constexpr int kBK = 16;
+constexpr int kPad = 4;  // keeps 16-byte shared loads aligned, store conflicts two-way
+
+__device__ __forceinline__ const float* row_of(const RowBlocks& m, int r) {
+  const int b = r / m.rows;
+  return m.p[b] + static_cast<int64_t>(r - b * m.rows) * m.ld;
+}
+
+// One 16-byte piece of an operand's [ROWS x kBK] tile into registers: piece i of
+// the tile is 4 values along the operand's contiguous dimension.
+template <int ROWS, bool MN>
+__device__ __forceinline__ float4 load_piece(const RowBlocks& m, int i, int r0, int rows, int k0, int k1) {
+  const int r = r0 + (MN ? i % (ROWS / 4) * 4 : i / (kBK / 4));
+  const int k = k0 + (MN ? i / (ROWS / 4) : i % (kBK / 4) * 4);
+  if (r >= rows || k >= k1) return make_float4(0.f, 0.f, 0.f, 0.f);
+  return *reinterpret_cast<const float4*>(MN ? row_of(m, k) + r : row_of(m, r) + k);
+}
+template <int ROWS, bool MN>
+__device__ __forceinline__ void store_piece(float (*s)[ROWS + kPad], int i, const float4& v) {
+  if constexpr (MN) {
+    *reinterpret_cast<float4*>(&s[i / (ROWS / 4)][i % (ROWS / 4) * 4]) = v;
+  } else {
+    const int r = i / (kBK / 4), k = i % (kBK / 4) * 4;
+    s[k][r] = v.x;
+    s[k + 1][r] = v.y;
+    s[k + 2][r] = v.z;
+    s[k + 3][r] = v.w;
+  }
+}
+
+template <int TM, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(256, 2) fma_gemm_kernel(const __grid_constant__ FmaGemm g, int tiles_n, int k_split,
+                                                          float* part) {
+  tpd::pdl_entry();
+  constexpr int BM = 16 * TM;
+  constexpr int APIECES = BM * kBK / 4, ALOADS = (APIECES + 255) / 256, BLOADS = kBN * kBK / 4 / 256;
+  __shared__ __align__(16) float sA[2][kBK][BM + kPad];
+  __shared__ __align__(16) float sB[2][kBK][kBN + kPad];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int mt = static_cast<int>(blockIdx.x) / tiles_n, nt = static_cast<int>(blockIdx.x) - mt * tiles_n;
+  const int m0 = mt * BM, n0 = nt * kBN;
+  const int k0 = static_cast<int>(blockIdx.y) * k_split, k1 = min(g.K, k0 + k_split);
+
+  float acc[TM][8];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+
+  float4 ra[ALOADS], rb[BLOADS];
+  auto load = [&](int kb) {
+#pragma unroll
+    for (int l = 0; l < ALOADS; ++l)
+      if (APIECES % 256 == 0 || tid + l * 256 < APIECES) ra[l] = load_piece<BM, A_MN>(g.A, tid + l * 256, m0, g.M, kb, k1);
+#pragma unroll
+    for (int l = 0; l < BLOADS; ++l) rb[l] = load_piece<kBN, B_MN>(g.B, tid + l * 256, n0, g.N, kb, k1);
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int l = 0; l < ALOADS; ++l)
+      if (APIECES % 256 == 0 || tid + l * 256 < APIECES) store_piece<BM, A_MN>(sA[buf], tid + l * 256, ra[l]);
+#pragma unroll
+    for (int l = 0; l < BLOADS; ++l) store_piece<kBN, B_MN>(sB[buf], tid + l * 256, rb[l]);
+  };
+  load(k0);
+  store(0);
+  __syncthreads();
+  int buf = 0;
+  for (int kb = k0; kb < k1; kb += kBK) {
+    if (kb + kBK < k1) load(kb + kBK);
+#pragma unroll
+    for (int k = 0; k < kBK; ++k) {
+      float a[TM], b[8];
+      if constexpr (TM == 8) {
+        const float4 u = *reinterpret_cast<const float4*>(&sA[buf][k][ty * 4]);
+        const float4 v = *reinterpret_cast<const float4*>(&sA[buf][k][BM / 2 + ty * 4]);
+        a[0] = u.x; a[1] = u.y; a[2] = u.z; a[3] = u.w;
+        a[4] = v.x; a[5] = v.y; a[6] = v.z; a[7] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = sA[buf][k][ty * TM + i];
+      }
+      const float4 u = *reinterpret_cast<const float4*>(&sB[buf][k][tx * 4]);
+      const float4 v = *reinterpret_cast<const float4*>(&sB[buf][k][kBN / 2 + tx * 4]);
+      b[0] = u.x; b[1] = u.y; b[2] = u.z; b[3] = u.w;
+      b[4] = v.x; b[5] = v.y; b[6] = v.z; b[7] = v.w;
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    if (kb + kBK < k1) store(buf ^ 1);
+    __syncthreads();  // the next block is in place, and this one has been read
+    buf ^= 1;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + (TM == 8 ? (i / 4) * (BM / 2) + ty * 4 + i % 4 : ty * TM + i);
+    if (m >= g.M) continue;
+    float* row = part ? part + (static_cast<int64_t>(blockIdx.y) * g.M + m) * g.N : const_cast<float*>(row_of(g.D, m));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int n = n0 + q * (kBN / 2) + tx * 4;
+      if (n >= g.N) continue;
+      float4 v = make_float4(acc[i][q * 4], acc[i][q * 4 + 1], acc[i][q * 4 + 2], acc[i][q * 4 + 3]);
+      if (g.add && !part) {
+        const float4 o = *reinterpret_cast<const float4*>(row + n);
+        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+      }
+      *reinterpret_cast<float4*>(row + n) = v;
+    }
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = 148;
+  }
+  return n;
+}
+
+// Rows per tile (32 for at most 64 rows of D, else 128), and the K split that
+// brings the launch nearest to two CTAs per SM (at most 16, at least 128 of K each).
+struct Shape {
+  int tm, tiles_n, tiles, splits, k_split;
+};
+Shape shape_of(const FmaGemm& g) {
+  Shape s{};
+  s.tm = g.M <= 64 ? 2 : 8;
+  s.tiles_n = (g.N + kBN - 1) / kBN;
+  s.tiles = (g.M + 16 * s.tm - 1) / (16 * s.tm) * s.tiles_n;
+  const int want = g.add ? 1 : std::max(1, 2 * sm_count() / s.tiles);
+  int n = std::max(1, std::min({want, TP_MAX_SHARDS, g.K / 128}));
+  s.k_split = ((g.K + n - 1) / n + kBK - 1) / kBK * kBK;
+  s.splits = (g.K + s.k_split - 1) / s.k_split;
+  return s;
+}
+
+}  // namespace
+
+namespace tpi {
+
+size_t fma_gemm_scratch(const FmaGemm& g) {
+  const Shape s = shape_of(g);
+  return s.splits > 1 ? static_cast<size_t>(s.splits) * g.M * g.N * sizeof(float) : 0;
+}
+
+tp_status launch_fma_gemm(const FmaGemm& g, float* part, cudaStream_t st) {
+  const Shape s = shape_of(g);
+  float* p = s.splits > 1 ? part : nullptr;
+  const dim3 grid(static_cast<unsigned>(s.tiles), static_cast<unsigned>(s.splits));
+#define TP_FMA(TM, AM, BM) (void)launch(fma_gemm_kernel<TM, AM, BM>, grid, dim3(256), 0, st, g, s.tiles_n, s.k_split, p)
+#define TP_FMA_TM(AM, BM)                 \
+  do {                                    \
+    if (s.tm == 2) TP_FMA(2, AM, BM);     \
+    else TP_FMA(8, AM, BM);               \
+  } while (0)
+  if (!g.a_mn && !g.b_mn) TP_FMA_TM(false, false);
+  else if (!g.a_mn) TP_FMA_TM(false, true);
+  else if (g.b_mn) TP_FMA_TM(true, true);
+  else return fail(TP_ERR_ARG, "fp32 GEMM: operand layouts");
+#undef TP_FMA_TM
+#undef TP_FMA
+  TP_TRY(after_launch("fma_gemm"));
+  if (!p) return TP_OK;
+  PtrArray P{};
+  MutPtrArray out{};
+  for (int i = 0; i < s.splits; ++i) P.p[i] = p + static_cast<size_t>(i) * g.M * g.N;
+  const int blocks = (g.M + g.D.rows - 1) / g.D.rows;
+  for (int i = 0; i < blocks; ++i) out.p[i] = const_cast<float*>(g.D.p[i]);
+  return launch_reduce(P, s.splits, nullptr, nullptr, PtrArray{}, false, out, blocks > 1, blocks, g.M, g.N, TP_F32, TP_F32,
+                       st);
+}
+
+}  // namespace tpi

@@ -325,6 +325,24 @@ tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cuda
 // fp32 FMA path (tp_gemm_simt.cu): the same epilogues, grouping and K concatenation.
 tp_status launch_gemm_f32(const GemmBatch& b, cudaStream_t st);
 
+// fp32 GEMM over matrices in blocks of rows (tp_gemm_fma.cu): row r of a matrix
+// is p[r / rows] + (r % rows) * ld. D [M, N] (+)= A . B^T with A, B as in
+// GemmProblem (a K-major operand's rows are its M or N index, an MN-major one's
+// its K index); contiguous extents and strides multiples of 4, pointers 16-byte
+// aligned; D's blocks are all of `rows` rows, dense when K is split.
+struct RowBlocks {
+  const float* p[TP_MAX_SHARDS];
+  int64_t ld;
+  int rows;
+};
+struct FmaGemm {
+  int M, N, K;
+  RowBlocks A, B, D;
+  bool a_mn, b_mn, add;
+};
+size_t fma_gemm_scratch(const FmaGemm& g);  // bytes of `part`
+tp_status launch_fma_gemm(const FmaGemm& g, float* part, cudaStream_t st);
+
 // Peer-memory steps (tp_peer.cu): validation of a peer group, and the flag
 // raise that follows a grid which wrote into other ranks' memory.
 tp_status check_peer_group(const tp_peer_group* g);

@@ -212,18 +212,82 @@ int64_t pick_chunk(int64_t T, int64_t Vp, int64_t h, double score_bytes, bool dw
 
 namespace tpi {
 
+// fp32 plans: the chunk's scores in fp32, a row kernel, and the FMA GEMM for the
+// three products (the shards are blocks of rows of one matrix).
+static tp_status linear_ce_f32(tp_plan* plan, int64_t T, const float* X, const PtrArray& W, const int32_t* labels,
+                               float scale, float* loss, float* lse, float* dX, const MutPtrArray& dW, int64_t chunk,
+                               unsigned* status, cudaStream_t st) {
+  const int p = plan->p, h = plan->hidden, V = plan->vocab, Vp = plan->vocab_padded, Vs = Vp / p;
+  const bool dw = dW.p[0] != nullptr, grad = dX || dw;
+  const int64_t Tc = pick_chunk(T, Vp, h, 4.0, false, chunk), nch = (T + Tc - 1) / Tc;
+  auto plain = [](const float* a, int64_t ld) {
+    RowBlocks m{};
+    m.p[0] = a;
+    m.ld = ld;
+    m.rows = 0x7fffffff;
+    return m;
+  };
+  auto shards = [&](const void* const* a) {
+    RowBlocks m{};
+    for (int i = 0; i < p; ++i) m.p[i] = static_cast<const float*>(a[i]);
+    m.ld = h;
+    m.rows = Vs;
+    return m;
+  };
+  auto scores = [&](float* z, int64_t t0, int64_t n) {
+    return FmaGemm{static_cast<int>(n), Vp, h, plain(X + t0 * h, h), shards(W.p), plain(z, Vp), false, false, false};
+  };
+  auto dx_gemm = [&](float* d, int64_t t0, int64_t n) {
+    FmaGemm g{static_cast<int>(n), h, Vp, plain(d, Vp), shards(W.p), plain(dX + t0 * h, h), false, true, false};
+    g.D.rows = g.M;
+    return g;
+  };
+  auto dw_gemm = [&](float* d, int64_t t0, int64_t n) {
+    return FmaGemm{Vp, h, static_cast<int>(n), plain(d, Vp), plain(X + t0 * h, h),
+                   shards(const_cast<const void* const*>(dW.p)), true, true, t0 > 0};
+  };
+  const size_t z_bytes = round256(static_cast<size_t>(Tc) * Vp * 4);
+  size_t part_bytes = 0;  // over the first (longest) and the last chunk
+  for (int64_t t0 : {static_cast<int64_t>(0), (nch - 1) * Tc}) {
+    const int64_t n = std::min(Tc, T - t0);
+    FmaGemm z = scores(nullptr, t0, n);
+    z.D.rows = z.M;
+    part_bytes = std::max(part_bytes, fma_gemm_scratch(z));
+    if (dX) part_bytes = std::max(part_bytes, fma_gemm_scratch(dx_gemm(nullptr, t0, n)));
+    if (dw) part_bytes = std::max(part_bytes, fma_gemm_scratch(dw_gemm(nullptr, t0, n)));
+  }
+  void* ws = nullptr;
+  TP_TRY(scratch(plan, z_bytes + part_bytes, st, &ws));
+  float* z = static_cast<float*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + z_bytes);
+  for (int64_t t0 = 0; t0 < T; t0 += Tc) {
+    const int64_t n = std::min(Tc, T - t0);
+    FmaGemm g = scores(z, t0, n);
+    g.D.rows = g.M;
+    TP_TRY(launch_fma_gemm(g, part, st));
+    (void)launch(ce_rows_kernel, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st, z, static_cast<int64_t>(Vp), V,
+                 labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr, grad ? z : nullptr, status);
+    TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
+    if (dX) TP_TRY(launch_fma_gemm(dx_gemm(z, t0, n), part, st));
+    if (dw) TP_TRY(launch_fma_gemm(dw_gemm(z, t0, n), part, st));
+  }
+  return TP_OK;
+}
+
 tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const PtrArray& W, const int32_t* labels,
                                  float scale, float* loss, float* lse, void* dX, const MutPtrArray& dW, int64_t chunk,
                                  cudaStream_t st) {
-  const bool bf = plan->dtype == TP_BF16;
-  const int p = plan->p, h = plan->hidden, V = plan->vocab, Vp = plan->vocab_padded, Vs = Vp / p;
-  const size_t es = dsize(plan->dtype);
-  const bool grad = dX || dW.p[0], dw = dW.p[0] != nullptr;
-  // without gradients a bf16 plan keeps 8 bytes per slot of at least 64 scores
-  const int64_t Tc = pick_chunk(T, Vp, h, !bf || grad ? static_cast<double>(es) : 0.125, bf && dw, chunk);
-  const int64_t nch = (T + Tc - 1) / Tc;
   unsigned* status = nullptr;
   TP_TRY(device_status_word(&status));
+  if (plan->dtype == TP_F32)
+    return linear_ce_f32(plan, T, static_cast<const float*>(X), W, labels, scale, loss, lse, static_cast<float*>(dX), dW,
+                         chunk, status, st);
+  const int p = plan->p, h = plan->hidden, V = plan->vocab, Vp = plan->vocab_padded, Vs = Vp / p;
+  constexpr size_t es = 2;
+  const bool grad = dX || dW.p[0], dw = dW.p[0] != nullptr;
+  // without gradients, 8 bytes are kept per slot of at least 64 scores
+  const int64_t Tc = pick_chunk(T, Vp, h, grad ? 2.0 : 0.125, dw, chunk);
+  const int64_t nch = (T + Tc - 1) / Tc;
 
   // products with d of a chunk of n tokens starting at token t0
   auto dx_batch = [&](const void* d, int64_t t0, int64_t n) {
@@ -231,7 +295,6 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.n = p;
     b.b_mn = true;
     b.epi = EPI_STORE;
-    b.out_f32 = !bf;
     b.kcat = true;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
@@ -252,7 +315,6 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.n = p;
     b.a_mn = b.b_mn = true;
     b.epi = EPI_STORE;
-    b.out_f32 = !bf;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
       g.M = Vs;
@@ -268,12 +330,11 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     return b;
   };
 
-  // the scores of a chunk: fp32 plans store them, bf16 plans their statistics
+  // the scores of a chunk, of which the statistics (and the exponentials) are kept
   auto score_batch = [&](void* out, int64_t t0, int64_t n) {
     GemmBatch b{};
     b.n = p;
-    b.epi = bf ? EPI_CE : EPI_STORE;
-    b.out_f32 = !bf;
+    b.epi = EPI_CE;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
       g.M = static_cast<int>(n);
@@ -291,14 +352,14 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     return b;
   };
   // slots of a row at most (narrow tiles of 128 columns have two of 64)
-  const int64_t max_slots = bf ? 2LL * p * ((Vs + 127) / 128) : 0;
+  const int64_t max_slots = 2LL * p * ((Vs + 127) / 128);
 
   // scratch: d (from the exponentials or scores) | statistics | fp32 sums of dW | split-K partials
-  const int sx = bf && dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 1;
-  const int sw = bf && dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
-  const size_t d_bytes = !bf || grad ? round256(static_cast<size_t>(Tc) * Vp * es) : 0;
+  const int sx = dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 1;
+  const int sw = dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
+  const size_t d_bytes = grad ? round256(static_cast<size_t>(Tc) * Vp * es) : 0;
   const size_t st_bytes = round256(static_cast<size_t>(Tc) * max_slots * sizeof(float2));
-  const size_t acc_bytes = bf && dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
+  const size_t acc_bytes = dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
   const size_t part_bytes = std::max(sx > 1 ? static_cast<size_t>(sx) * Tc * h * 4 : 0, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
   void* ws = nullptr;
   TP_TRY(scratch(plan, d_bytes + st_bytes + acc_bytes + part_bytes, st, &ws));
@@ -309,42 +370,27 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
 
   for (int64_t c = 0; c < nch; ++c) {
     const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
-    GemmBatch b = score_batch(!bf || grad ? db : nullptr, t0, n);
-    if (bf) {
-      const int tile = gemm_tile_cols(b);
-      const int shard_slots = 2 * ((Vs + tile - 1) / tile);
-      b.ce_stats = stats;
-      b.ce_slots = static_cast<int64_t>(p) * shard_slots;
-      TP_TRY(launch_gemm_bf16(b, st));
-      // a few rows: enough CTAs a row to fill the GPU with the second part
-      const int64_t parts = grad ? std::max<int64_t>(1, std::min<int64_t>(512 / n, Vp / 8 / kFinThreads)) : 1;
-      (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
-                   stats, static_cast<int>(b.ce_slots), tile, shard_slots,
-                   static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h, V, Vs, p, labels + t0, scale, loss + t0,
-                   lse ? lse + t0 : nullptr, grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
-    } else {
-      TP_TRY(launch_gemm_f32(b, st));
-      (void)launch(ce_rows_kernel, dim3(static_cast<unsigned>(n)), dim3(kRowThreads), 0, st,
-                   reinterpret_cast<const float*>(db), static_cast<int64_t>(Vp), V, labels + t0, scale, loss + t0,
-                   lse ? lse + t0 : nullptr, grad ? reinterpret_cast<float*>(db) : nullptr, status);
-    }
+    GemmBatch b = score_batch(grad ? db : nullptr, t0, n);
+    const int tile = gemm_tile_cols(b);
+    const int shard_slots = 2 * ((Vs + tile - 1) / tile);
+    b.ce_stats = stats;
+    b.ce_slots = static_cast<int64_t>(p) * shard_slots;
+    TP_TRY(launch_gemm_bf16(b, st));
+    // a few rows: enough CTAs a row to fill the GPU with the second part
+    const int64_t parts = grad ? std::max<int64_t>(1, std::min<int64_t>(512 / n, Vp / 8 / kFinThreads)) : 1;
+    (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
+                 stats, static_cast<int>(b.ce_slots), tile, shard_slots, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
+                 V, Vs, p, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
+                 grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
     TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
     if (dX) {
       const GemmBatch x = dx_batch(db, t0, n);
-      if (!bf) TP_TRY(launch_gemm_f32(x, st));
-      else if (sx > 1) TP_TRY(launch_gemm_cat_split(x, sx, part, st));
+      if (sx > 1) TP_TRY(launch_gemm_cat_split(x, sx, part, st));
       else TP_TRY(launch_gemm_bf16(x, st));
     }
     if (dw) {
       GemmBatch w = dw_batch(db, t0, n);
-      if (!bf) {  // the fp32 output is its own running sum
-        if (c > 0)
-          for (int i = 0; i < p; ++i) {
-            w.g[i].aux = w.g[i].D;
-            w.g[i].ldaux = h;
-          }
-        TP_TRY(launch_gemm_f32(w, st));
-      } else if (sw > 1) {
+      if (sw > 1) {
         TP_TRY(launch_gemm_split(w, sw, part, st));
       } else {
         for (int i = 0; nch > 1 && i < p; ++i) {
