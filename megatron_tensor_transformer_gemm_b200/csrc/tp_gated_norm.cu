@@ -33,6 +33,28 @@ struct Vec16 {
       f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
     }
   }
+  // The same as N / 2 pairs of fp32, each in one 64-bit register.
+  __device__ static void unpack(const uint4 u, uint64_t (&f)[N / 2]) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = tpd::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+      f[0] = tpd::f2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
+      f[1] = tpd::f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+  }
+  __device__ static uint4 pack(const uint64_t (&f)[N / 2]) {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 a = tpd::f2_unpack(f[i]);
+      v[2 * i] = a.x;
+      v[2 * i + 1] = a.y;
+    }
+    return pack(v);
+  }
   __device__ static uint4 pack(const float (&f)[N]) {
     if constexpr (sizeof(T) == 2)
       return make_uint4(tpd::pack_bf16x2(f[0], f[1]), tpd::pack_bf16x2(f[2], f[3]), tpd::pack_bf16x2(f[4], f[5]),
@@ -42,11 +64,11 @@ struct Vec16 {
   }
 };
 
-// Sum over the CTA, the same in every thread. `red` has two halves used in turn
+// Sum over the THREADS threads of a row (a warp, or the CTA), the same in every one. `red` has two halves used in turn
 // (`turn` counts the sums), so one barrier a sum is enough: a half is written
 // again only after the barrier of the sum in between.
 template <int THREADS>
-__device__ __forceinline__ float block_sum(float v, float* red, int& turn) {
+__device__ __forceinline__ float row_sum(float v, float* red, int& turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (THREADS == 32) return v;
@@ -63,8 +85,8 @@ __device__ __forceinline__ float block_sum(float v, float* red, int& turn) {
 // tid + i * THREADS): the mean, then the mean square about it, two exact passes
 // over the registers (RMSNorm: the second only, about zero).
 template <typename T, int THREADS, int VPT, bool RMS>
-__device__ __forceinline__ void row_stats(const uint4 (&v)[VPT], int vpr, float inv_h, float* red, int& turn, float& mean,
-                                          float& rstd) {
+__device__ __forceinline__ void row_stats(const uint4 (&v)[VPT], int tid, int vpr, float inv_h, float* red, int& turn,
+                                          float& mean, float& rstd) {
   constexpr int N = Vec16<T>::N;
   mean = 0.f;
   if (!RMS) {
@@ -76,29 +98,34 @@ __device__ __forceinline__ void row_stats(const uint4 (&v)[VPT], int vpr, float 
 #pragma unroll
       for (int e = 0; e < N; ++e) s += x[e];
     }
-    mean = block_sum<THREADS>(s, red, turn) * inv_h;
+    mean = row_sum<THREADS>(s, red, turn) * inv_h;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (threadIdx.x + i * THREADS < vpr) {
+    if (tid + i * THREADS < vpr) {
       float x[N];
       Vec16<T>::unpack(v[i], x);
 #pragma unroll
       for (int e = 0; e < N; ++e) q += (x[e] - mean) * (x[e] - mean);
     }
   }
-  rstd = rsqrtf(block_sum<THREADS>(q, red, turn) * inv_h + kEps);
+  rstd = rsqrtf(row_sum<THREADS>(q, red, turn) * inv_h + kEps);
 }
 
-// One CTA per row; the row of x and of f stay packed in registers from their
-// one load to the stores, so the two norms cost no extra pass over memory.
+// A warp per row (four rows a CTA) up to 128 vectors, else a CTA per row; the
+// row of x and of f stay packed in registers from their one load to the stores,
+// so the two norms cost no extra pass over memory. Bound by HBM: 32768 x 4096 bf16
+// LayerNorm, both norms and a gate, in 177 us, 6.0 TB/s (a copy: 6.5).
+constexpr int kWarpRows = 4;
 template <typename T, int THREADS, int VPT, bool RMS>
-__global__ void __launch_bounds__(THREADS) gated_norm_fwd_kernel(const __grid_constant__ GatedNorm p) {
+__global__ void __launch_bounds__(THREADS == 32 ? 32 * kWarpRows : THREADS) gated_norm_fwd_kernel(const __grid_constant__ GatedNorm p) {
   tpd::pdl_entry();
   constexpr int N = Vec16<T>::N;
   __shared__ float red[2 * (THREADS / 32)];
-  const int64_t r = blockIdx.x;
+  const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t r = THREADS == 32 ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (THREADS == 32 && r >= p.rows) return;
   const int vpr = static_cast<int>(p.h / N);
   const float inv_h = 1.f / static_cast<float>(p.h);
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + r * p.h);
@@ -109,7 +136,7 @@ __global__ void __launch_bounds__(THREADS) gated_norm_fwd_kernel(const __grid_co
   uint4 fv[VPT], xv[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = threadIdx.x + i * THREADS;
+    const int c = tid + i * THREADS;
     fv[i] = xv[i] = make_uint4(0, 0, 0, 0);
     if (c < vpr) {
       fv[i] = __ldcs(f + c);
@@ -118,15 +145,15 @@ __global__ void __launch_bounds__(THREADS) gated_norm_fwd_kernel(const __grid_co
   }
   float mean = 0.f, rstd = 1.f;
   if (p.post_g) {
-    row_stats<T, THREADS, VPT, RMS>(fv, vpr, inv_h, red, turn, mean, rstd);
-    if (p.stats && threadIdx.x == 0) {
+    row_stats<T, THREADS, VPT, RMS>(fv, tid, vpr, inv_h, red, turn, mean, rstd);
+    if (p.stats && tid == 0) {
       if (!RMS) p.stats[r] = mean;
       p.stats[p.rows + r] = rstd;
     }
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = threadIdx.x + i * THREADS;
+    const int c = tid + i * THREADS;
     if (c >= vpr) continue;
     float a[N], b[N], w[N];
     Vec16<T>::unpack(fv[i], a);
@@ -152,14 +179,14 @@ __global__ void __launch_bounds__(THREADS) gated_norm_fwd_kernel(const __grid_co
     reinterpret_cast<uint4*>(static_cast<T*>(p.x_out) + r * p.h)[c] = xv[i];
   }
   if (!p.pre_g) return;
-  row_stats<T, THREADS, VPT, RMS>(xv, vpr, inv_h, red, turn, mean, rstd);
-  if (p.stats && threadIdx.x == 0) {
+  row_stats<T, THREADS, VPT, RMS>(xv, tid, vpr, inv_h, red, turn, mean, rstd);
+  if (p.stats && tid == 0) {
     if (!RMS) p.stats[2 * p.rows + r] = mean;
     p.stats[3 * p.rows + r] = rstd;
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = threadIdx.x + i * THREADS;
+    const int c = tid + i * THREADS;
     if (c >= vpr) continue;
     float a[N], w[N];
     Vec16<T>::unpack(xv[i], a);
@@ -183,7 +210,7 @@ __global__ void __launch_bounds__(THREADS) gated_norm_fwd_kernel(const __grid_co
 // parameter gradients; A = sum D xh1 and S = sum D, kept per gate row, give the
 // gate's (g1 A + b1 S) and the post-norm's (sum over gate rows of g A, g S).
 //
-// Persistent CTAs: the tokens in gate-row-major order (position q = b * n + j is
+// Persistent CTAs: the tokens in gate-row-major order (position q = b * per + j is
 // token j * gate_rows + b) are cut into one contiguous range per CTA, so a CTA
 // sums A and S over runs of one gate row and writes a run's sums once; the run
 // of CTA c and gate row b has slot c + b, since both only grow along the order.
@@ -196,58 +223,122 @@ __device__ __forceinline__ int64_t range_lo(int64_t rows, int64_t G, int64_t c) 
 // The CTA whose range holds position q.
 __device__ __forceinline__ int64_t range_of(int64_t rows, int64_t G, int64_t q) { return ((q + 1) * G - 1) / rows; }
 
-// Sum of a pair over the CTA (or the CL CTAs of a cluster that share a row) and
-// whether every thread's wait succeeded; one barrier, buffers used in turn.
-template <int THREADS, int CL>
-__device__ __forceinline__ bool pair_sum(float2& v, bool ok, float4* red, int& turn, uint32_t rank) {
-  constexpr int W = THREADS / 32;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+// A walk over positions without divisions: gate row b, index j in its run, token
+// t. 32 bits: there are fewer than 2^31 rows.
+struct Walk {
+  int b, j, t;
+  __device__ __forceinline__ void start(int64_t q, int64_t per, int B) {
+    b = static_cast<int>(q / per);
+    j = static_cast<int>(q - b * per);
+    t = static_cast<int>(static_cast<int64_t>(j) * B + b);
   }
-  const bool all = __all_sync(0xffffffffu, ok);
-  float4* half = red + (turn++ & 1) * (W * CL);
-  if ((threadIdx.x & 31) == 0) {
-    const float4 mine = make_float4(v.x, v.y, all ? 0.f : 1.f, 0.f);
-    float4* slot = half + rank * W + (threadIdx.x >> 5);
-    *slot = mine;
-    if (CL == 2) {
-      const uint32_t far = tpd::map_shared(tpd::smem_u32(slot), rank ^ 1u);
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(far), "f"(mine.x), "f"(mine.y), "f"(mine.z),
-                   "f"(mine.w)
-                   : "memory");
+  __device__ __forceinline__ void next(int per, int B) {
+    t += B;
+    if (++j == per) {
+      j = 0;
+      t = ++b;
     }
   }
-  if (CL == 2) tpd::cluster_sync_all();
-  else __syncthreads();
-  float bad = 0.f;
-  v = make_float2(0.f, 0.f);
+};
+template <typename T>
+__device__ __forceinline__ void unpack_shared(uint32_t addr, uint64_t (&f)[Vec16<T>::N / 2]) {
+  Vec16<T>::unpack(tpd::ld_shared_v4(addr), f);
+}
+// The backward's arithmetic runs on pairs of fp32 (one instruction for two
+// columns); each lane rounds as the scalar operation does.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float a) { return tpd::f2_pack(a, a); }
+__device__ __forceinline__ float sum2(uint64_t a) {
+  const float2 f = tpd::f2_unpack(a);
+  return f.x + f.y;
+}
+// N fp32 values of one vector of a row as one or two 16-byte pieces `apart` bytes apart.
+template <int N>
+__device__ __forceinline__ void store_f32(uint32_t addr, uint32_t apart, const uint64_t (&v)[N / 2]) {
 #pragma unroll
-  for (int w = 0; w < W * CL; ++w) {
-    const float4 t = half[w];
-    v.x += t.x;
-    v.y += t.y;
-    bad += t.z;
-  }
-  return bad == 0.f;
+  for (int i = 0; i < N / 4; ++i)
+    asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(addr + i * apart), "l"(v[2 * i]), "l"(v[2 * i + 1]) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void load_f32(uint32_t addr, uint32_t apart, uint64_t (&v)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2 * i]), "=l"(v[2 * i + 1]) : "r"(addr + i * apart) : "memory");
 }
 
-template <typename T, int THREADS, int VPT, int CL, bool RMS>
-__global__ void __launch_bounds__(THREADS) gated_norm_bwd_kernel(const __grid_constant__ GatedNorm p, int64_t G, int narr,
-                                                                 int vec_cta, unsigned* status) {
+// Sum of a pair over the CTA (or the CL CTAs of a cluster that share a row) and
+// whether every thread's wait succeeded; one barrier, buffers used in turn.
+// Slots past the CTA's last warp hold zeros, so the loop needs no count.
+template <int MAXT, int CL>
+__device__ __forceinline__ bool pair_sum(float2& v, bool ok, float2* red, int& turn, uint32_t rank) {
+  constexpr int MAXW = MAXT / 32;
+  uint64_t t = tpd::f2_pack(v.x, v.y);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t = tpd::add2(t, __shfl_xor_sync(0xffffffffu, t, o));
+  v = tpd::f2_unpack(t);
+  float2* half = red + (turn++ & 1) * (MAXW * CL + 2);
+  float2* slot = half + rank * MAXW + (threadIdx.x >> 5);
+  if (CL == 1) {
+    if ((threadIdx.x & 31) == 0) *slot = v;
+    if (__syncthreads_or(!ok)) return false;
+  } else {
+    // the flags of the two CTAs sit behind the pairs: any failed wait of a row
+    // marks its CTA's flag in both
+    float2* flag = half + CL * MAXW + rank;
+    const bool bad = __syncthreads_or(!ok);
+    if ((threadIdx.x & 31) == 0) {
+      *slot = v;
+      const uint32_t far = tpd::map_shared(tpd::smem_u32(slot), rank ^ 1u);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(far), "f"(v.x), "f"(v.y) : "memory");
+    }
+    if (threadIdx.x == 0) {
+      const float f = bad ? 1.f : 0.f;
+      *flag = make_float2(f, f);
+      const uint32_t far = tpd::map_shared(tpd::smem_u32(flag), rank ^ 1u);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %1};" ::"r"(far), "f"(f) : "memory");
+    }
+    tpd::cluster_sync_all();
+    if (half[CL * MAXW].x + half[CL * MAXW + 1].x != 0.f) return false;
+  }
+  uint64_t a = 0, b = 0;
+#pragma unroll
+  for (int w = 0; w < MAXW * CL; w += 2) {  // two slots a load
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(half + w);
+    a = tpd::add2(a, u.x);
+    b = tpd::add2(b, u.y);
+  }
+  v = tpd::f2_unpack(tpd::add2(a, b));
+  return true;
+}
+
+// ALL: a pre-norm, a post-norm, a gate and dx_out are all there (the usual
+// junction); the other instances test for each.
+template <typename T, int MAXT, int VPT, int CL, bool RMS, bool ALL>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm_bwd_kernel(const __grid_constant__ GatedNorm p, int64_t G, int narr,
+                                                              int vec_cta, unsigned* status) {
   constexpr int N = Vec16<T>::N;
   extern __shared__ __align__(128) uint8_t sbuf[];
   __shared__ uint64_t bar[kStages];
   __shared__ int abort_flag;
-  __shared__ float4 red[2 * CL * (THREADS / 32)];
+  __shared__ __align__(16) float2 red[2 * (CL * (MAXT / 32) + 2)];
   const uint32_t rank = CL == 2 ? tpd::cluster_ctarank() : 0u;
   const int64_t cta = blockIdx.x / CL;
+  const int nth = blockDim.x;
   const int vpr = static_cast<int>(p.h / N);
   const int v0 = static_cast<int>(rank) * vec_cta;              // this CTA's vectors of a row
   const int nv = min(vec_cta, vpr - v0);
   const uint32_t slice = static_cast<uint32_t>(nv) * 16u;
   const float inv_h = 1.f / static_cast<float>(p.h);
+  for (int i = threadIdx.x; i < 2 * (CL * (MAXT / 32) + 2); i += nth) red[i] = make_float2(0.f, 0.f);
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < kStages; ++s) tpd::mbar_init(&bar[s], 1);
@@ -257,360 +348,442 @@ __global__ void __launch_bounds__(THREADS) gated_norm_bwd_kernel(const __grid_co
   if (CL == 2) tpd::cluster_sync_all();  // the peer runs before its shared memory is written
   tpd::pdl_entry();
 
-  const bool pre = p.pre_g != nullptr, post = p.post_g != nullptr, use_f = post || p.gate;
-  const int64_t lo = range_lo(p.rows, G, cta), hi = range_lo(p.rows, G, cta + 1);
-  const int64_t B = p.gate ? p.gate_rows : 1, per = p.rows / B;
-  auto token = [&](int64_t q) { const int64_t b = q / per; return (q - b * per) * B + b; };
+  const bool pre = ALL || p.pre_g != nullptr, post = ALL || p.post_g != nullptr, gated = ALL || p.gate != nullptr;
+  const bool has_dx = ALL || p.dx_out != nullptr, use_f = post || gated;
+  const int64_t lo = range_lo(p.rows, G, cta);
+  const int count = static_cast<int>(range_lo(p.rows, G, cta + 1) - lo);  // rows of this CTA
+  const int B = gated ? static_cast<int>(p.gate_rows) : 1, per = static_cast<int>(p.rows) / B;
   // arrays of a stage, in order of presence: dx_out, then x_out and dy, then f
-  const int o_dx = 0, o_x = (p.dx_out ? 1 : 0), o_f = o_x + (pre ? 2 : 0);
+  const int o_x = has_dx ? 1 : 0, o_f = o_x + (pre ? 2 : 0);
   const uint32_t arr = static_cast<uint32_t>(vec_cta) * 16u, stage_bytes = arr * narr;
-  auto issue = [&](int64_t q) {  // thread 0
-    const int s = static_cast<int>((q - lo) % kStages);
-    const int64_t off = token(q) * p.h + static_cast<int64_t>(v0) * N;
-    uint8_t* dst = sbuf + static_cast<size_t>(s) * stage_bytes;
-    tpd::mbar_arrive_expect_tx(&bar[s], slice * narr);
-    if (p.dx_out) tpd::bulk_load(dst, static_cast<const T*>(p.dx_out) + off, slice, &bar[s]);
+  Walk at;
+  at.start(lo, per, B);
+  // thread 0's: the next row to load and its stage, rows whose loads are not issued
+  __shared__ Walk ahead;
+  __shared__ int in_stage, to_issue;
+  auto issue = [&]() {  // thread 0
+    Walk w = ahead;
+    const int64_t off = w.t * p.h + static_cast<int64_t>(v0) * N;
+    uint8_t* dst = sbuf + static_cast<uint32_t>(in_stage) * stage_bytes;
+    uint64_t* br = &bar[in_stage];
+    tpd::mbar_arrive_expect_tx(br, slice * narr);
+    if (has_dx) tpd::bulk_load(dst, static_cast<const T*>(p.dx_out) + off, slice, br);
     if (pre) {
-      tpd::bulk_load(dst + o_x * arr, static_cast<const T*>(p.x_in) + off, slice, &bar[s]);
-      tpd::bulk_load(dst + (o_x + 1) * arr, static_cast<const T*>(p.dy) + off, slice, &bar[s]);
+      tpd::bulk_load(dst + o_x * arr, static_cast<const T*>(p.x_in) + off, slice, br);
+      tpd::bulk_load(dst + (o_x + 1) * arr, static_cast<const T*>(p.dy) + off, slice, br);
     }
-    if (use_f) tpd::bulk_load(dst + o_f * arr, static_cast<const T*>(p.f) + off, slice, &bar[s]);
+    if (use_f) tpd::bulk_load(dst + o_f * arr, static_cast<const T*>(p.f) + off, slice, br);
+    w.next(per, B);
+    ahead = w;
+    --to_issue;
+    in_stage = in_stage + 1 == kStages ? 0 : in_stage + 1;
   };
-  int64_t issued = lo;
-  if (threadIdx.x == 0)
-    for (; issued < hi && issued < lo + kStages; ++issued) issue(issued);
+  if (threadIdx.x == 0) {
+    ahead = at;
+    in_stage = 0;
+    to_issue = count;
+    for (int s = 0; s < kStages && to_issue > 0; ++s) issue();
+    if (rank == 0 && use_f) p.runs[cta] = make_int2(at.b, static_cast<int>((lo + count - 1) / per));
+  }
 
-  uint4 g2[VPT], w1[VPT], gw[VPT];  // pre-norm weight, post-norm weight, gate row
-  float P[VPT][N], Q[VPT][N], A[VPT][N], S[VPT][N];
+  uint4 g2[VPT];     // pre-norm weight
+  // The gate row times the post-norm's weight: in registers for RMSNorm, else
+  // behind the stages (LayerNorm's four column sums leave no room), as is a row's
+  // a = that times D, which otherwise replaces the stage's x_out and dy. Each
+  // thread reads only what it wrote there itself.
+  uint64_t w1[RMS ? VPT : 1][N / 2];
+  const uint32_t s_w = tpd::smem_u32(sbuf) + kStages * stage_bytes;
+  const uint32_t s_a = s_w + (RMS ? 0u : arr * (N / 4));
+  uint64_t P[VPT][N / 2], Q[VPT][N / 2], A[VPT][N / 2], S[VPT][N / 2];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = threadIdx.x + i * THREADS;
-    g2[i] = w1[i] = gw[i] = make_uint4(0, 0, 0, 0);
+    const int c = threadIdx.x + i * nth;
+    g2[i] = make_uint4(0, 0, 0, 0);
     if (c < nv && pre) g2[i] = static_cast<const uint4*>(p.pre_g)[v0 + c];
-    if (c < nv && post) w1[i] = static_cast<const uint4*>(p.post_g)[v0 + c];
 #pragma unroll
-    for (int e = 0; e < N; ++e) P[i][e] = Q[i][e] = A[i][e] = S[i][e] = 0.f;
+    for (int e = 0; e < N / 2; ++e) P[i][e] = Q[i][e] = A[i][e] = S[i][e] = 0;
   }
-  // A run of one gate row ends: its sums to slot cta + b.
-  auto flush = [&](int64_t b) {
-    float* out = p.seg + (cta + b) * 2 * p.h;
+  auto write_sums = [&](float* out, uint64_t (&first)[VPT][N / 2], uint64_t (&second)[VPT][N / 2]) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = threadIdx.x + i * THREADS;
+      const int c = threadIdx.x + i * nth;
       if (c < nv) {
+        float* to = out + static_cast<int64_t>(v0 + c) * N;
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          float* at = out + static_cast<int64_t>(v0 + c) * N + e;
-          *reinterpret_cast<float4*>(at) = make_float4(A[i][e], A[i][e + 1], A[i][e + 2], A[i][e + 3]);
-          if (!RMS) *reinterpret_cast<float4*>(at + p.h) = make_float4(S[i][e], S[i][e + 1], S[i][e + 2], S[i][e + 3]);
+        for (int e = 0; e < N / 2; e += 2) {
+          *reinterpret_cast<ulonglong2*>(to + 2 * e) = make_ulonglong2(first[i][e], first[i][e + 1]);
+          if (!RMS) *reinterpret_cast<ulonglong2*>(to + p.h + 2 * e) = make_ulonglong2(second[i][e], second[i][e + 1]);
         }
       }
 #pragma unroll
-      for (int e = 0; e < N; ++e) A[i][e] = S[i][e] = 0.f;
+      for (int e = 0; e < N / 2; ++e) first[i][e] = second[i][e] = 0;
     }
   };
 
-  int turn = 0;
-  int64_t run = -1;  // gate row of the current run
-  float st_m1 = 0.f, st_r1 = 1.f, st_m2 = 0.f, st_r2 = 1.f;
-  auto load_stats = [&](int64_t t) {
+  int turn = 0, s = 0;
+  uint32_t phase = 0;
+  int run = -1;  // gate row of the current run
+  // the row's statistics as xh = x * r + c
+  float r1 = 1.f, c1 = 0.f, r2 = 1.f, c2 = 0.f;
+  auto load_stats = [&](int t) {
     if (post) {
-      if (!RMS) st_m1 = p.stats[t];
-      st_r1 = p.stats[p.rows + t];
+      r1 = p.stats[p.rows + t];
+      if (!RMS) c1 = -p.stats[t] * r1;
     }
     if (pre) {
-      if (!RMS) st_m2 = p.stats[2 * p.rows + t];
-      st_r2 = p.stats[3 * p.rows + t];
+      r2 = p.stats[3 * p.rows + t];
+      if (!RMS) c2 = -p.stats[2 * p.rows + t] * r2;
     }
   };
-  if (lo < hi) load_stats(token(lo));
+  load_stats(at.t);  // every CTA has a row (G <= rows)
   bool good = true;
-  for (int64_t q = lo; q < hi; ++q) {
-    const int64_t k = q - lo, t = token(q), b = q / per;
-    const int s = static_cast<int>(k % kStages);
-    if (b != run) {
-      if (run >= 0 && use_f) flush(run);
-      run = b;
-      if (p.gate) {
+  for (int left = count; left > 0; --left) {
+    const int64_t row_at = at.t * p.h + static_cast<int64_t>(v0) * N;  // this CTA's part of the row
+    if (at.b != run) {
+      if (run >= 0 && use_f) write_sums(p.seg + (cta + run) * 2 * p.h, A, S);
+      run = at.b;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int c = threadIdx.x + i * THREADS;
-          if (c < nv)
-            gw[i] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.gate) + b * p.h)[v0 + c];
+      for (int i = 0; i < VPT; ++i) {
+        const int c = threadIdx.x + i * nth;
+        uint64_t wv[N / 2];
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) wv[e] = both(1.f);
+        if (c < nv && gated)
+          Vec16<T>::unpack(reinterpret_cast<const uint4*>(static_cast<const T*>(p.gate) + run * p.h)[v0 + c], wv);
+        if (c < nv && post) {
+          uint64_t w[N / 2];
+          Vec16<T>::unpack(static_cast<const uint4*>(p.post_g)[v0 + c], w);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) wv[e] = mul2(wv[e], w[e]);
+        }
+        if constexpr (RMS) {
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) w1[i][e] = wv[e];
+        } else if (c < nv) {
+          store_f32<N>(s_w + c * 16, arr, wv);
         }
       }
     }
-    const float mean1 = st_m1, rstd1 = st_r1, mean2 = st_m2, rstd2 = st_r2;
-    if (q + 1 < hi) load_stats(token(q + 1));  // a row early
+    const float R1 = r1, C1 = c1, R2 = r2, C2 = c2;
+    at.next(per, B);
+    if (left > 1) load_stats(at.t);  // a row early
     // a wait that gave up computes on an unfinished stage; the sum below then
     // stops every thread of the row before anything is written
-    const bool ok = tpd::mbar_wait(&bar[s], static_cast<uint32_t>(k / kStages) & 1u, &abort_flag, status);
-    const uint8_t* stage = sbuf + static_cast<size_t>(s) * stage_bytes;
-    const uint4* s_dx = reinterpret_cast<const uint4*>(stage + o_dx * arr);
-    const uint4* s_x = reinterpret_cast<const uint4*>(stage + o_x * arr);
-    const uint4* s_dy = reinterpret_cast<const uint4*>(stage + (o_x + 1) * arr);
-    const uint4* s_f = reinterpret_cast<const uint4*>(stage + o_f * arr);
-    float2 m = make_float2(0.f, 0.f);
+    const bool ok = tpd::mbar_wait(&bar[s], phase, &abort_flag, status);
+    const uint32_t s_dx = tpd::smem_u32(sbuf) + static_cast<uint32_t>(s) * stage_bytes;
+    const uint32_t s_x = s_dx + o_x * arr, s_dy = s_x + arr, s_f = s_dx + o_f * arr;
+    if (++s == kStages) {
+      s = 0;
+      phase ^= 1u;
+    }
+    uint64_t mx = 0, my = 0;
     if (pre) {
+      const uint64_t r = both(R2), k = both(C2);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = threadIdx.x + i * THREADS;
+        const int c = threadIdx.x + i * nth;
         if (c < nv) {
-          float x[N], d[N], w[N];
-          Vec16<T>::unpack(s_x[c], x);
-          Vec16<T>::unpack(s_dy[c], d);
+          uint64_t x[N / 2], d[N / 2], w[N / 2];
+          unpack_shared<T>(s_x + c * 16, x);
+          unpack_shared<T>(s_dy + c * 16, d);
           Vec16<T>::unpack(g2[i], w);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float xh = (x[e] - mean2) * rstd2, gy = d[e] * w[e];
-            if (!RMS) m.x += gy;
-            m.y = fmaf(gy, xh, m.y);
-            P[i][e] = fmaf(d[e], xh, P[i][e]);
-            if (!RMS) Q[i][e] += d[e];
+          for (int e = 0; e < N / 2; ++e) {
+            const uint64_t xh = RMS ? mul2(x[e], r) : fma2(x[e], r, k), gy = mul2(d[e], w[e]);
+            if (!RMS) mx = tpd::add2(mx, gy);
+            my = fma2(gy, xh, my);
+            P[i][e] = fma2(d[e], xh, P[i][e]);
+            if (!RMS) Q[i][e] = tpd::add2(Q[i][e], d[e]);
           }
         }
       }
     }
-    good = pair_sum<THREADS, CL>(m, ok, red, turn, rank);
+    float2 m = make_float2(RMS ? 0.f : sum2(mx), sum2(my));
+    good = pair_sum<MAXT, CL>(m, ok, red, turn, rank);
     if (!good) break;
     // every thread is past the row before this one: its stage takes a new row
-    if (threadIdx.x == 0 && k >= 1 && issued < hi) issue(issued++);
-    m.x *= inv_h;
-    m.y *= inv_h;
-    float a[VPT][N];
-    float2 u = make_float2(0.f, 0.f);
+    if (threadIdx.x == 0 && left < count && to_issue > 0) issue();
+    // D = dx_out + R2 (gy - m1 - xh m2), with xh = x R2 + C2 folded into x's factor
+    const float m1 = m.x * inv_h, m2 = m.y * inv_h;
+    const uint64_t fx = both(-R2 * m2 * R2), f0 = both(-R2 * fmaf(C2, m2, m1)), fr = both(R2), rs = both(p.rs);
+    const uint64_t r1v = both(R1), c1v = both(C1);
+    const uint32_t at_a = pre ? s_x : s_a;
+    uint64_t ux = 0, uy = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = threadIdx.x + i * THREADS;
+      const int c = threadIdx.x + i * nth;
       if (c >= nv) continue;
-      float D[N], o[N];
+      uint64_t D[N / 2], o[N / 2];
 #pragma unroll
-      for (int e = 0; e < N; ++e) D[e] = 0.f;
-      if (p.dx_out) Vec16<T>::unpack(s_dx[c], D);
+      for (int e = 0; e < N / 2; ++e) D[e] = 0;
+      if (has_dx) unpack_shared<T>(s_dx + c * 16, D);
       if (pre) {
-        float x[N], d[N], w[N];
-        Vec16<T>::unpack(s_x[c], x);
-        Vec16<T>::unpack(s_dy[c], d);
+        uint64_t x[N / 2], d[N / 2], w[N / 2];
+        unpack_shared<T>(s_x + c * 16, x);
+        unpack_shared<T>(s_dy + c * 16, d);
         Vec16<T>::unpack(g2[i], w);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float xh = (x[e] - mean2) * rstd2;
-          D[e] = fmaf(rstd2, d[e] * w[e] - (RMS ? 0.f : m.x) - xh * m.y, D[e]);
+        for (int e = 0; e < N / 2; ++e) {
+          const uint64_t v = RMS ? D[e] : tpd::add2(D[e], f0);
+          D[e] = fma2(x[e], fx, fma2(mul2(d[e], w[e]), fr, v));
         }
       }
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = p.rs * D[e];
-      reinterpret_cast<uint4*>(static_cast<T*>(p.dx) + t * p.h)[v0 + c] = Vec16<T>::pack(o);
-      float x[N], w[N];
+      for (int e = 0; e < N / 2; ++e) o[e] = mul2(rs, D[e]);
+      reinterpret_cast<uint4*>(static_cast<T*>(p.dx) + row_at)[c] = Vec16<T>::pack(o);
+      uint64_t x[N / 2];
       if (use_f) {
-        Vec16<T>::unpack(s_f[c], x);
+        unpack_shared<T>(s_f + c * 16, x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          x[e] = (x[e] - mean1) * rstd1;
-          A[i][e] = fmaf(D[e], x[e], A[i][e]);
-          if (!RMS) S[i][e] += D[e];
+        for (int e = 0; e < N / 2; ++e) {
+          x[e] = RMS ? mul2(x[e], r1v) : fma2(x[e], r1v, c1v);
+          A[i][e] = fma2(D[e], x[e], A[i][e]);
+          if (!RMS) S[i][e] = tpd::add2(S[i][e], D[e]);
         }
       }
-      if (p.gate) {
-        Vec16<T>::unpack(gw[i], w);
+      if constexpr (RMS) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) D[e] *= w[e];
+        for (int e = 0; e < N / 2; ++e) D[e] = mul2(D[e], w1[i][e]);
+      } else {
+        uint64_t w[N / 2];
+        load_f32<N>(s_w + c * 16, arr, w);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) D[e] = mul2(D[e], w[e]);
       }
       if (post) {
-        Vec16<T>::unpack(w1[i], w);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          D[e] *= w[e];
-          if (!RMS) u.x += D[e];
-          u.y = fmaf(D[e], x[e], u.y);
+        for (int e = 0; e < N / 2; ++e) {
+          if (!RMS) ux = tpd::add2(ux, D[e]);
+          uy = fma2(D[e], x[e], uy);
         }
       }
-#pragma unroll
-      for (int e = 0; e < N; ++e) a[i][e] = D[e];
+      store_f32<N>(at_a + c * 16, arr, D);
     }
+    uint64_t fu = 0, fc = 0;
     if (post) {
-      good = pair_sum<THREADS, CL>(u, true, red, turn, rank);
-      u.x *= inv_h;
-      u.y *= inv_h;
+      float2 u = make_float2(RMS ? 0.f : sum2(ux), sum2(uy));
+      good = pair_sum<MAXT, CL>(u, true, red, turn, rank);
+      // df = R1 (a - u1 - xh u2), xh = f R1 + C1
+      const float u1 = u.x * inv_h, u2 = u.y * inv_h;
+      fu = both(-R1 * u2 * R1);
+      fc = both(RMS ? 0.f : -R1 * fmaf(C1, u2, u1));
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = threadIdx.x + i * THREADS;
+      const int c = threadIdx.x + i * nth;
       if (c >= nv) continue;
+      uint64_t o[N / 2];
+      load_f32<N>(at_a + c * 16, arr, o);
       if (post) {
-        float x[N];
-        Vec16<T>::unpack(s_f[c], x);
+        uint64_t x[N / 2];
+        unpack_shared<T>(s_f + c * 16, x);
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          a[i][e] = rstd1 * (a[i][e] - (RMS ? 0.f : u.x) - (x[e] - mean1) * rstd1 * u.y);
+        for (int e = 0; e < N / 2; ++e)
+          o[e] = fma2(x[e], fu, RMS ? mul2(o[e], r1v) : fma2(o[e], r1v, fc));
       }
-      reinterpret_cast<uint4*>(static_cast<T*>(p.df) + t * p.h)[v0 + c] = Vec16<T>::pack(a[i]);
+      reinterpret_cast<uint4*>(static_cast<T*>(p.df) + row_at)[c] = Vec16<T>::pack(o);
     }
   }
   if (good) {
-    if (run >= 0 && use_f) flush(run);
-    if (pre) {
-      float* out = p.cta_part + cta * 2 * p.h;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = threadIdx.x + i * THREADS;
-        if (c < nv) {
-#pragma unroll
-          for (int e = 0; e < N; e += 4) {
-            float* at = out + static_cast<int64_t>(v0 + c) * N + e;
-            *reinterpret_cast<float4*>(at) = make_float4(P[i][e], P[i][e + 1], P[i][e + 2], P[i][e + 3]);
-            if (!RMS) *reinterpret_cast<float4*>(at + p.h) = make_float4(Q[i][e], Q[i][e + 1], Q[i][e + 2], Q[i][e + 3]);
-          }
-        }
-      }
-    }
+    if (use_f) write_sums(p.seg + (cta + run) * 2 * p.h, A, S);
+    if (pre) write_sums(p.cta_part + cta * 2 * p.h, P, Q);
   } else if (threadIdx.x == 0) {
-    // let the loads still in flight land (bounded) before the CTA exits
-    for (int s = 0; s < kStages; ++s) {
+    // let the loads still in flight land (bounded) before the CTA exits: stage i
+    // holds the last issued row whose index is i mod kStages
+    const int n = count - to_issue;
+    for (int i = 0; i < kStages && i < n; ++i) {
       int again = 0;
-      const int64_t n = issued - lo;  // rows issued; stage s holds the last with index = s mod kStages
-      if (n > s) {
-        const int64_t last = s + (n - 1 - s) / kStages * kStages;
-        tpd::mbar_wait(&bar[s], static_cast<uint32_t>(last / kStages) & 1u, &again, nullptr, 1000000ull);
-      }
+      const int last = i + (n - 1 - i) / kStages * kStages;
+      tpd::mbar_wait(&bar[i], static_cast<uint32_t>(last / kStages) & 1u, &again, nullptr, 1000000ull);
     }
   }
   if (CL == 2) tpd::cluster_sync_all();  // neither CTA leaves while its peer may still write to it
 }
 
 // The column sums of the backward, each in a fixed order: a block owns 32
-// columns, warp w takes CTAs w, w + 8, ... and the warps' sums are added in
-// order. blockIdx.y = 0: the norms' parameters (and a single gate row);
-// blockIdx.y = b + 1: gate row b of several.
-constexpr int kSumWarps = 8;
+// columns, eight lanes of four, and its kSumRows groups of eight lanes take CTAs
+// g, g + kSumRows, ...; the groups' sums are added in order. blockIdx.y = 0: the
+// norms' parameters (and a single gate row); blockIdx.y = b + 1: gate row b of
+// several.
+constexpr int kSumRows = 64;
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+}
 template <typename T>
-__global__ void __launch_bounds__(32 * kSumWarps) gated_norm_sums_kernel(const __grid_constant__ GatedNorm p, int64_t G, int rms) {
+__device__ __forceinline__ float4 four(const void* v, int64_t at) {
+  const T* s = static_cast<const T*>(v) + at;
+  return make_float4(static_cast<float>(s[0]), static_cast<float>(s[1]), static_cast<float>(s[2]), static_cast<float>(s[3]));
+}
+template <typename T, bool RMS>
+__global__ void __launch_bounds__(8 * kSumRows) gated_norm_sums_kernel(const __grid_constant__ GatedNorm p, int64_t G) {
   tpd::pdl_entry();
-  __shared__ float red[6][kSumWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  __shared__ float4 red[kSumRows][8];
+  const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;  // group and its lane
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * 8 + lane) * 4;
   const int64_t B = p.gate ? p.gate_rows : 1, per = p.rows / B;
-  const bool use_f = p.post_g || p.gate;
-  const bool all = blockIdx.y == 0;
-  float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // P, Q, sum of g A, of g S, A, S
-  if (col < p.h) {
-    int64_t c0 = 0, c1 = G;
-    if (!all) {
-      c0 = range_of(p.rows, G, (blockIdx.y - 1) * per);
-      c1 = range_of(p.rows, G, blockIdx.y * per - 1) + 1;
-    }
+  const bool use_f = p.post_g || p.gate, all = blockIdx.y == 0, in = col < p.h;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v[6];  // P, Q, sum of g A, of g S, A, S
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = zero;
+  int64_t c0 = 0, c1 = G;
+  if (!all) {
+    c0 = range_of(p.rows, G, (blockIdx.y - 1) * per);
+    c1 = range_of(p.rows, G, blockIdx.y * per - 1) + 1;
+  }
+  if (in) {
+    if (all && p.pre_g) {
 #pragma unroll 4
-    for (int64_t c = c0 + warp; c < c1; c += kSumWarps) {
-      if (all && p.pre_g) {
-        v[0] += p.cta_part[(c * 2) * p.h + col];
-        if (!rms) v[1] += p.cta_part[(c * 2 + 1) * p.h + col];
+      for (int64_t c = group; c < G; c += kSumRows) {
+        const float* s = p.cta_part + c * 2 * p.h + col;
+        add4(v[0], *reinterpret_cast<const float4*>(s));
+        if (!RMS) add4(v[1], *reinterpret_cast<const float4*>(s + p.h));
       }
-      if (use_f) {
-        int64_t b0 = range_lo(p.rows, G, c) / per, b1 = (range_lo(p.rows, G, c + 1) - 1) / per;
-        if (!all) b0 = b1 = blockIdx.y - 1;
-        for (int64_t b = b0; b <= b1; ++b) {
-          const float A = p.seg[((c + b) * 2) * p.h + col], S = rms ? 0.f : p.seg[((c + b) * 2 + 1) * p.h + col];
-          if (all) {
-            const float g = p.gate ? static_cast<float>(static_cast<const T*>(p.gate)[b * p.h + col]) : 1.f;
-            v[2] = fmaf(g, A, v[2]);
-            v[3] = fmaf(g, S, v[3]);
+    }
+    if (use_f && (!all || B == 1)) {
+      const int64_t b = all ? 0 : blockIdx.y - 1;
+#pragma unroll 4
+      for (int64_t c = c0 + group; c < c1; c += kSumRows) {
+        const float* s = p.seg + (c + b) * 2 * p.h + col;
+        add4(v[4], *reinterpret_cast<const float4*>(s));
+        if (!RMS) add4(v[5], *reinterpret_cast<const float4*>(s + p.h));
+      }
+    } else if (use_f && p.dpost_g) {  // several gate rows, weighted
+      for (int64_t c = group; c < G; c += kSumRows) {
+        const int2 r = p.runs[c];
+        for (int b = r.x; b <= r.y; ++b) {
+          const float* s = p.seg + (c + b) * 2 * p.h + col;
+          const float4 A = *reinterpret_cast<const float4*>(s), g = four<T>(p.gate, b * p.h + col);
+          v[2].x = fmaf(g.x, A.x, v[2].x); v[2].y = fmaf(g.y, A.y, v[2].y);
+          v[2].z = fmaf(g.z, A.z, v[2].z); v[2].w = fmaf(g.w, A.w, v[2].w);
+          if (!RMS) {
+            const float4 S = *reinterpret_cast<const float4*>(s + p.h);
+            v[3].x = fmaf(g.x, S.x, v[3].x); v[3].y = fmaf(g.y, S.y, v[3].y);
+            v[3].z = fmaf(g.z, S.z, v[3].z); v[3].w = fmaf(g.w, S.w, v[3].w);
           }
-          v[4] += A;
-          v[5] += S;
         }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 6; ++i) red[i][warp][lane] = v[i];
-  __syncthreads();
-  if (warp != 0 || col >= p.h) return;
-#pragma unroll
   for (int i = 0; i < 6; ++i) {
-    v[i] = red[i][0][lane];
-#pragma unroll
-    for (int w = 1; w < kSumWarps; ++w) v[i] += red[i][w][lane];
+    if (RMS && (i & 1)) continue;
+    red[group][lane] = v[i];
+    __syncthreads();
+    if (group == 0)
+#pragma unroll 8
+      for (int w = 1; w < kSumRows; ++w) add4(v[i], red[w][lane]);
+    __syncthreads();
   }
+  if (group != 0 || !in) return;
+  if (all && B == 1 && use_f) {  // one gate row: its weight once, after the sum
+    const float4 g = p.gate ? four<T>(p.gate, col) : make_float4(1.f, 1.f, 1.f, 1.f);
+    v[2] = make_float4(g.x * v[4].x, g.y * v[4].y, g.z * v[4].z, g.w * v[4].w);
+    v[3] = make_float4(g.x * v[5].x, g.y * v[5].y, g.z * v[5].z, g.w * v[5].w);
+  }
+  auto put = [&](float* out, const float4& s) {
+    if (out) *reinterpret_cast<float4*>(out + col) = s;
+  };
   if (all) {
-    if (p.dpre_g) p.dpre_g[col] = v[0];
-    if (p.dpre_b && !rms) p.dpre_b[col] = v[1];
-    if (p.dpost_g) p.dpost_g[col] = v[2];
-    if (p.dpost_b && !rms) p.dpost_b[col] = v[3];
+    put(p.dpre_g, v[0]);
+    put(p.dpost_g, v[2]);
+    if (!RMS) {
+      put(p.dpre_b, v[1]);
+      put(p.dpost_b, v[3]);
+    }
   }
   if (p.dgate && (all ? B == 1 : true)) {
-    const float g1 = p.post_g ? static_cast<float>(static_cast<const T*>(p.post_g)[col]) : 1.f;
-    const float b1 = p.post_g && !rms ? static_cast<float>(static_cast<const T*>(p.post_b)[col]) : 0.f;
-    p.dgate[(all ? 0 : blockIdx.y - 1) * p.h + col] = g1 * v[4] + b1 * v[5];
+    const float4 g = p.post_g ? four<T>(p.post_g, col) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 b = p.post_g && !RMS ? four<T>(p.post_b, col) : zero;
+    put(p.dgate + (all ? 0 : (blockIdx.y - 1) * p.h),
+        make_float4(g.x * v[4].x + b.x * v[5].x, g.y * v[4].y + b.y * v[5].y, g.z * v[4].z + b.z * v[5].z,
+                    g.w * v[4].w + b.w * v[5].w));
   }
 }
 
 // ---------------------------------------------------------------- dispatch
 // Threads and vectors per thread of the forward, by the row's 16-byte vectors.
-template <typename T, bool RMS>
+template <typename T, int THREADS, int VPT, bool RMS>
 void launch_fwd(const GatedNorm& p, cudaStream_t st) {
+  const int64_t ctas = THREADS == 32 ? (p.rows + kWarpRows - 1) / kWarpRows : p.rows;
+  (void)tpi::launch(gated_norm_fwd_kernel<T, THREADS, VPT, RMS>, dim3(static_cast<unsigned>(ctas)),
+                    dim3(THREADS == 32 ? 32 * kWarpRows : THREADS), 0, st, p);
+}
+template <typename T, bool RMS>
+void dispatch_fwd(const GatedNorm& p, cudaStream_t st) {
   const int64_t v = p.h * static_cast<int64_t>(sizeof(T)) / 16;
-  const dim3 grid(static_cast<unsigned>(p.rows));
-  if (v <= 32) (void)tpi::launch(gated_norm_fwd_kernel<T, 32, 1, RMS>, grid, dim3(32), 0, st, p);
-  else if (v <= 64) (void)tpi::launch(gated_norm_fwd_kernel<T, 64, 1, RMS>, grid, dim3(64), 0, st, p);
-  else if (v <= 128) (void)tpi::launch(gated_norm_fwd_kernel<T, 128, 1, RMS>, grid, dim3(128), 0, st, p);
-  else if (v <= 256) (void)tpi::launch(gated_norm_fwd_kernel<T, 128, 2, RMS>, grid, dim3(128), 0, st, p);
-  else if (v <= 512) (void)tpi::launch(gated_norm_fwd_kernel<T, 128, 4, RMS>, grid, dim3(128), 0, st, p);
-  else if (v <= 1024) (void)tpi::launch(gated_norm_fwd_kernel<T, 256, 4, RMS>, grid, dim3(256), 0, st, p);
-  else (void)tpi::launch(gated_norm_fwd_kernel<T, 256, 8, RMS>, grid, dim3(256), 0, st, p);
+  if (v <= 32) launch_fwd<T, 32, 1, RMS>(p, st);
+  else if (v <= 64) launch_fwd<T, 32, 2, RMS>(p, st);
+  else if (v <= 128) launch_fwd<T, 32, 4, RMS>(p, st);
+  else if (v <= 256) launch_fwd<T, 64, 4, RMS>(p, st);
+  else if (v <= 512) launch_fwd<T, 128, 4, RMS>(p, st);
+  else if (v <= 1024) launch_fwd<T, 256, 4, RMS>(p, st);
+  else launch_fwd<T, 512, 4, RMS>(p, st);
 }
 
-template <typename T, int THREADS, int VPT, int CL, bool RMS>
+constexpr int kMinRows = 4;
+template <typename T, int MAXT, int VPT, int CL, bool RMS, bool ALL>
 tp_status launch_bwd(tp_plan* plan, GatedNorm p, cudaStream_t st) {
   constexpr int N = Vec16<T>::N;
-  auto kernel = gated_norm_bwd_kernel<T, THREADS, VPT, CL, RMS>;
+  auto kernel = gated_norm_bwd_kernel<T, MAXT, VPT, CL, RMS, ALL>;
   const int vpr = static_cast<int>(p.h / N), vec_cta = (vpr + CL - 1) / CL;
+  const int threads = std::min(MAXT, ((vec_cta + VPT - 1) / VPT + 31) / 32 * 32);
   const bool pre = p.pre_g != nullptr, use_f = p.post_g || p.gate;
   const int narr = (p.dx_out ? 1 : 0) + (pre ? 2 : 0) + (use_f ? 1 : 0);
-  const int smem = kStages * narr * vec_cta * 16;
+  // the stages; LayerNorm's fp32 weights; without a pre-norm, the row's a
+  const int smem = (kStages * narr + (RMS ? 0 : N / 4) + (pre ? 0 : N / 4)) * vec_cta * 16;
   unsigned* status = nullptr;
   TP_TRY(tpi::device_status_word(&status));
   int64_t grid = 1;
-  TP_TRY(tpi::persistent_grid(reinterpret_cast<const void*>(kernel), THREADS, smem, p.rows * CL, &grid));
+  // at least kMinRows rows a CTA: below that the partial sums outweigh the rows
+  TP_TRY(tpi::persistent_grid(reinterpret_cast<const void*>(kernel), threads, smem,
+                              (p.rows + kMinRows - 1) / kMinRows * CL, &grid));
   const int64_t G = std::max<int64_t>(1, grid / CL);
   const int64_t B = p.gate ? p.gate_rows : 1;
   const size_t seg = use_f ? static_cast<size_t>(G + B - 1) * 2 * p.h * sizeof(float) : 0;
   const size_t part = pre ? static_cast<size_t>(G) * 2 * p.h * sizeof(float) : 0;
   void* ws = nullptr;
-  TP_TRY(tpi::scratch(plan, seg + part + 16, st, &ws));
+  TP_TRY(tpi::scratch(plan, seg + part + G * sizeof(int2), st, &ws));
   p.seg = static_cast<float*>(ws);
   p.cta_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + seg);
+  p.runs = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + seg + part);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(G * CL));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CL;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = tpi::pdl_enabled() ? 2 : 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  const bool pdl = tpi::pdl_enabled();
+  cfg.attrs = pdl ? attr : attr + 1;
+  cfg.numAttrs = (pdl ? 1 : 0) + (CL > 1 ? 1 : 0);
   TP_TRY(tpi::cuda_status(cudaLaunchKernelEx(&cfg, kernel, p, G, narr, vec_cta, status), "gated_residual_norm_bwd"));
   TP_TRY(tpi::after_launch("gated_residual_norm_bwd"));
-  if (!(p.dgate || p.dpost_g || p.dpre_g)) return TP_OK;
+  if (!(p.dgate || p.dpost_g || p.dpost_b || p.dpre_g || p.dpre_b)) return TP_OK;
   const dim3 g2(static_cast<unsigned>((p.h + 31) / 32), p.dgate && B > 1 ? static_cast<unsigned>(B + 1) : 1u);
-  (void)tpi::launch(gated_norm_sums_kernel<T>, g2, dim3(32 * kSumWarps), 0, st, p, G, RMS ? 1 : 0);
+  (void)tpi::launch(gated_norm_sums_kernel<T, RMS>, g2, dim3(8 * kSumRows), 0, st, p, G);
   return tpi::after_launch("gated_residual_norm_bwd/sums");
 }
 
 // By the row's 16-byte vectors: up to two per thread, so the column sums stay in
 // registers; rows past 1024 vectors are shared by a cluster of two CTAs.
-template <typename T, bool RMS>
+template <typename T, bool RMS, bool ALL>
 tp_status dispatch_bwd(tp_plan* plan, const GatedNorm& p, cudaStream_t st) {
   const int64_t v = p.h * static_cast<int64_t>(sizeof(T)) / 16;
-  if (v <= 64) return launch_bwd<T, 64, 1, 1, RMS>(plan, p, st);
-  if (v <= 128) return launch_bwd<T, 128, 1, 1, RMS>(plan, p, st);
-  if (v <= 256) return launch_bwd<T, 256, 1, 1, RMS>(plan, p, st);
-  if (v <= 512) return launch_bwd<T, 256, 2, 1, RMS>(plan, p, st);
-  if (v <= 1024) return launch_bwd<T, 512, 2, 1, RMS>(plan, p, st);
-  return launch_bwd<T, 512, 2, 2, RMS>(plan, p, st);
+  if (v <= 128) return launch_bwd<T, 64, 2, 1, RMS, ALL>(plan, p, st);
+  if (v <= 256) return launch_bwd<T, 128, 2, 1, RMS, ALL>(plan, p, st);
+  if (v <= 512) return launch_bwd<T, 256, 2, 1, RMS, ALL>(plan, p, st);
+  if (v <= 1024) return launch_bwd<T, 512, 2, 1, RMS, ALL>(plan, p, st);
+  return launch_bwd<T, 512, 2, 2, RMS, ALL>(plan, p, st);
+}
+template <typename T, bool RMS>
+tp_status dispatch_bwd(tp_plan* plan, const GatedNorm& p, cudaStream_t st) {
+  return p.dx_out && p.pre_g && p.post_g && p.gate ? dispatch_bwd<T, RMS, true>(plan, p, st)
+                                                    : dispatch_bwd<T, RMS, false>(plan, p, st);
 }
 
 }  // namespace
@@ -619,11 +792,11 @@ namespace tpi {
 
 tp_status launch_gated_norm_fwd(const GatedNorm& p, bool rms, tp_dtype dt, cudaStream_t st) {
   if (dt == TP_BF16) {
-    if (rms) launch_fwd<__nv_bfloat16, true>(p, st);
-    else launch_fwd<__nv_bfloat16, false>(p, st);
+    if (rms) dispatch_fwd<__nv_bfloat16, true>(p, st);
+    else dispatch_fwd<__nv_bfloat16, false>(p, st);
   } else {
-    if (rms) launch_fwd<float, true>(p, st);
-    else launch_fwd<float, false>(p, st);
+    if (rms) dispatch_fwd<float, true>(p, st);
+    else dispatch_fwd<float, false>(p, st);
   }
   return after_launch("gated_residual_norm_fwd");
 }

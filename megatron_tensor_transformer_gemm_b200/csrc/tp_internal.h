@@ -194,12 +194,13 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
 
 // The junction of two sublayers (tp_gated_norm.cu): pointers as in
 // tp_gated_residual_norm_fwd / _bwd, NULL where absent; x_in is the backward's
-// x_out. The launchers set seg and cta_part.
+// x_out. The launchers set seg, cta_part and runs.
 struct GatedNorm {
   const void *x, *f, *gate, *post_g, *post_b, *pre_g, *pre_b, *x_in, *dx_out, *dy;
   void *x_out, *y, *dx, *df;
   float *stats, *dgate, *dpost_g, *dpost_b, *dpre_g, *dpre_b;
   float *seg, *cta_part;
+  int2* runs;
   int64_t rows, h, gate_rows;
   float rs;
 };
