@@ -225,57 +225,61 @@ def _arr(ts: Sequence | None):
     return (ctypes.c_void_p * len(vals))(*vals)
 
 
+# The current stream's handle without a Stream object around it (0.3 us in
+# place of 4 on the host, of a call that may run for 5).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cuda = False  # whether CUDA is known to be available
+
+
 def _stream(stream=None) -> int | None:
+    global _cuda
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.is_available():
-        return torch.cuda.current_stream().cuda_stream
-    return None
+    if not _cuda:
+        _cuda = torch.cuda.is_available()
+        if not _cuda:
+            return None
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 DTYPES = {"bf16": TP_BF16, "f32": TP_F32}
 
 
-def _want(name: str, t, shape: tuple, *dtypes) -> None:
-    """ValueError unless t is a dense tensor of that shape and one of the dtypes (None is not checked)."""
+def _use(dev: int, name: str, t, shape: tuple, *dtypes) -> int | None:
+    """The address of t, a dense tensor of that shape and one of the dtypes on device `dev` (-1:
+    the CPU), else ValueError; None for None."""
     if t is None:
-        return
-    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a dense {list(shape)} tensor of {' or '.join(map(str, dtypes))}, "
-                         f"got {list(t.shape)} of {t.dtype}" + ("" if t.is_contiguous() else ", not contiguous"))
+        return None
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != dev:
+        where = "the CPU" if dev < 0 else f"cuda:{dev}"
+        raise ValueError(f"{name}: expected a dense {list(shape)} tensor of {' or '.join(map(str, dtypes))} on {where}, "
+                         f"got {list(t.shape)} of {t.dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
 
 
-def _want_shards(name: str, ts, p: int, shape: tuple, *dtypes) -> None:
+def _use_shards(dev: int, name: str, ts, p: int, shape: tuple, *dtypes):
+    """The same for a list of p shards: a host array of their addresses."""
     if ts is None:
-        return
+        return None
     if len(ts) != p:
         raise ValueError(f"{name}: expected {p} shards, got {len(ts)}")
     for i, t in enumerate(ts):
         if t is None:
             raise ValueError(f"{name}[{i}] is None")
-        _want(f"{name}[{i}]", t, shape, *dtypes)
+        if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != dev:
+            _use(dev, f"{name}[{i}]", t, shape, *dtypes)
+    return (ctypes.c_void_p * p)(*[t.data_ptr() for t in ts])
 
 
-class _device_of:
-    """The tensors' device made current for a call (kernels launch on the current
-    device); ValueError if they are not all on it."""
-
-    def __init__(self, first, *more):
-        self.index = first.device.index if first.is_cuda else None
-        self.back = None
-        for m in more:
-            for t in (m if isinstance(m, (list, tuple)) else (m,)):
-                if t is not None and t.device != first.device:
-                    raise ValueError(f"tensors on {first.device} and {t.device} in one call")
-
-    def __enter__(self):
-        if self.index is not None and self.index != torch.cuda.current_device():
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _on_device(dev: int, func: str, stream, *args) -> None:
+    """Call lib.<func>(*args, stream) with device `dev` current: kernels launch on the current device."""
+    if dev < 0 or dev == torch.cuda.current_device():
+        check(getattr(lib, func)(*args, _stream(stream)), func)
+    else:
+        with torch.cuda.device(dev):
+            check(getattr(lib, func)(*args, _stream(stream)), func)
 
 
 class Plan:
@@ -336,19 +340,14 @@ class Plan:
         """tp_vocab_linear_cross_entropy: the output head X W^T (W: vocab shards) and its
         softmax cross-entropy without the logits. dX / dW (both optional) receive the
         gradients of grad_scale * sum(loss). chunk: tokens at a time (0: chosen)."""
-        if getattr(self, "vocab_padded", 0):
-            dt, shard = self.torch_dtype, (self.vocab_padded // self.p, self.hidden)
-            _want("X", X, (T, self.hidden), dt)
-            _want("dX", dX, (T, self.hidden), dt)
-            _want("labels", labels, (T,), torch.int32)
-            _want("loss", loss, (T,), torch.float32)
-            _want("lse", lse, (T,), torch.float32)
-            _want_shards("W", W, self.p, shard, dt)
-            _want_shards("dW", dW, self.p, shard, dt)
-        with _device_of(X, W, labels, loss, lse, dX, dW):
-            check(lib.tp_vocab_linear_cross_entropy(self._h, T, _ptr(X), _arr(W), _ptr(labels), float(grad_scale),
-                                                    _ptr(loss), _ptr(lse), _ptr(dX), _arr(dW), int(chunk),
-                                                    _stream(stream)), "tp_vocab_linear_cross_entropy")
+        if not getattr(self, "vocab_padded", 0):
+            raise ValueError("the plan has no vocab: call set_vocab first")
+        dev, dt, p, h, f32 = X.get_device(), self.torch_dtype, self.p, self.hidden, torch.float32
+        shard = (self.vocab_padded // p, h)
+        _on_device(dev, "tp_vocab_linear_cross_entropy", stream, self._h, T, _use(dev, "X", X, (T, h), dt),
+                   _use_shards(dev, "W", W, p, shard, dt), _use(dev, "labels", labels, (T,), torch.int32),
+                   float(grad_scale), _use(dev, "loss", loss, (T,), f32), _use(dev, "lse", lse, (T,), f32),
+                   _use(dev, "dX", dX, (T, h), dt), _use_shards(dev, "dW", dW, p, shard, dt), int(chunk))
 
     def describe(self) -> str:
         buf = ctypes.create_string_buffer(4096)
@@ -386,23 +385,18 @@ class Plan:
         k, n = self.ffn // self.p, 2 if self.act == "swiglu" else 1
         return (T, n * k), (n * -(-k // 32), T)
 
-    def _check_ckpt8(self, T, Zq, Zs, W, W_shape, H):
+    def _use_ckpt8(self, dev, T, Zq, Zs, H):
         codes, scales = self.ckpt8_shapes(T)
-        _want_shards("W", W, self.p, W_shape, self.torch_dtype)
-        _want_shards("Zq", Zq, self.p, codes, torch.float8_e4m3fn, torch.uint8)
-        _want_shards("Zs", Zs, self.p, scales, torch.uint8)
-        _want_shards("H", H, self.p, (T, self.ffn // self.p), self.torch_dtype)
-        return codes[1]
+        return (_use_shards(dev, "Zq", Zq, self.p, codes, torch.float8_e4m3fn, torch.uint8),
+                _use_shards(dev, "Zs", Zs, self.p, scales, torch.uint8),
+                _use_shards(dev, "H", H, self.p, (T, self.ffn // self.p), self.torch_dtype))
 
     def column_fwd_ckpt8(self, T, X, W, bias, Zq, Zs, H, stream=None):
         """tp_column_fwd_ckpt8: the MLP's column layer with Z kept as e4m3 codes Zq and scales Zs."""
-        n1 = self.ckpt8_shapes(T)[0][1]
-        self._check_ckpt8(T, Zq, Zs, W, (n1, self.hidden), H)
-        _want("X", X, (T, self.hidden), self.torch_dtype)
-        _want_shards("bias", bias, self.p, (n1,), self.torch_dtype)
-        with _device_of(X, W, bias, Zq, Zs, H):
-            check(lib.tp_column_fwd_ckpt8(self._h, T, _ptr(X), _arr(W), _arr(bias), _arr(Zq), _arr(Zs), _arr(H),
-                                          _stream(stream)), "tp_column_fwd_ckpt8")
+        dev, dt, p, h, n1 = X.get_device(), self.torch_dtype, self.p, self.hidden, self.ckpt8_shapes(T)[0][1]
+        _on_device(dev, "tp_column_fwd_ckpt8", stream, self._h, T, _use(dev, "X", X, (T, h), dt),
+                   _use_shards(dev, "W", W, p, (n1, h), dt), _use_shards(dev, "bias", bias, p, (n1,), dt),
+                   *self._use_ckpt8(dev, T, Zq, Zs, H))
 
     def row_fwd_partial(self, which, T, H, W, P, stream=None):
         check(lib.tp_row_fwd_partial(self._h, WHICH[which], T, _arr(H), _arr(W), _arr(P),
@@ -451,39 +445,35 @@ class Plan:
                                       _ptr(mean), _ptr(rstd), _arr(dX), _arr(dgamma), _arr(dbeta),
                                       _stream(stream)), "tp_norm_sharded_bwd")
 
-    def _check_junction(self, kind, rows, rows_of, weights, gate, dgate=None, sums=()):
+    def _junction_weights(self, dev, kind, gate, post, pre):
+        """Addresses (gate, gate_rows, gamma_post, beta_post, gamma_pre, beta_pre) of the junction's weights."""
         h, dt = self.hidden, self.torch_dtype
-        for name, t in rows_of:
-            _want(name, t, (rows, h), dt)
-        for name, pair in weights:
-            if pair is not None and kind == "layer" and pair[1] is None:
+        out = []
+        for name, pair in (("post", post), ("pre", pre)):
+            if pair is None:
+                out += (None, None)
+                continue
+            gamma, beta = pair
+            if beta is None and kind == "layer":
                 raise ValueError(f"{name}: LayerNorm needs (gamma, beta)")
-            for t in pair or ():
-                _want(name, t, (h,), dt)
-        for name, pair in sums:
-            for t in pair or ():
-                _want(name, t, (h,), torch.float32)
-        if gate is not None:
-            if gate.dim() != 2:
-                raise ValueError(f"gate: expected [gate_rows, {h}], got {list(gate.shape)}")
-            _want("gate", gate, (gate.shape[0], h), dt)
-            _want("dgate", dgate, (gate.shape[0], h), torch.float32)
+            out += (_use(dev, name, gamma, (h,), dt), _use(dev, name, beta, (h,), dt))
+        if gate is None:
+            return None, 0, *out
+        if gate.dim() != 2:
+            raise ValueError(f"gate: expected [gate_rows, {h}], got {list(gate.shape)}")
+        n = gate.shape[0]
+        return _use(dev, "gate", gate, (n, h), dt), n, *out
 
     def gated_residual_norm_fwd(self, kind, rows, x, f, x_out, y=None, *, res_scale=1.0, gate=None, post=None,
                                 pre=None, stats=None, stream=None):
         """tp_gated_residual_norm_fwd: x_out = res_scale * x + gate * Norm_post(f), y = Norm_pre(x_out).
         kind: "layer" or "rms"; post, pre: (gamma, beta) or None (beta may be None for "rms");
         gate [gate_rows, hidden]; stats [4, rows] fp32, kept for the backward."""
-        self._check_junction(kind, rows, (("x", x), ("f", f), ("x_out", x_out), ("y", y)),
-                             (("post", post), ("pre", pre)), gate)
-        _want("stats", stats, (4, rows), torch.float32)
-        pg, pb = post if post else (None, None)
-        qg, qb = pre if pre else (None, None)
-        with _device_of(x, f, x_out, y, gate, pg, pb, qg, qb, stats):
-            check(lib.tp_gated_residual_norm_fwd(
-                self._h, NORMS[kind], rows, _ptr(x), _ptr(f), float(res_scale), _ptr(gate),
-                0 if gate is None else gate.shape[0], _ptr(pg), _ptr(pb), _ptr(qg), _ptr(qb), _ptr(x_out), _ptr(y),
-                _ptr(stats), _stream(stream)), "tp_gated_residual_norm_fwd")
+        dev, dt, row = x.get_device(), self.torch_dtype, (rows, self.hidden)
+        _on_device(dev, "tp_gated_residual_norm_fwd", stream, self._h, NORMS[kind], rows, _use(dev, "x", x, row, dt),
+                   _use(dev, "f", f, row, dt), float(res_scale), *self._junction_weights(dev, kind, gate, post, pre),
+                   _use(dev, "x_out", x_out, row, dt), _use(dev, "y", y, row, dt),
+                   _use(dev, "stats", stats, (4, rows), torch.float32))
 
     def attention_fwd(self, batch, seq, QKV, O, LSE=None, stream=None):
         check(lib.tp_attention_fwd(self._h, batch, seq, _arr(QKV), _arr(O), _arr(LSE),
@@ -497,15 +487,12 @@ class Plan:
     def row_bwd_ckpt8(self, T, dY, W, Zq, Zs, H, dZ, dW=None, dbias=None, stream=None):
         """tp_row_bwd_ckpt8: the MLP's row backward from Zq, Zs; H (optional without dW) receives the
         recomputed activation."""
-        k = self.ffn // self.p
-        n1 = self._check_ckpt8(T, Zq, Zs, W, (self.hidden, k), H)
-        _want("dY", dY, (T, self.hidden), self.torch_dtype)
-        _want_shards("dZ", dZ, self.p, (T, n1), self.torch_dtype)
-        _want_shards("dW", dW, self.p, (self.hidden, k), self.torch_dtype)
-        _want("dbias", dbias, (self.hidden,), torch.float32)
-        with _device_of(dY, W, Zq, Zs, H, dZ, dW, dbias):
-            check(lib.tp_row_bwd_ckpt8(self._h, T, _ptr(dY), _arr(W), _arr(Zq), _arr(Zs), _arr(H), _arr(dZ), _arr(dW),
-                                       _ptr(dbias), _stream(stream)), "tp_row_bwd_ckpt8")
+        dev, dt, p, h, k = dY.get_device(), self.torch_dtype, self.p, self.hidden, self.ffn // self.p
+        n1 = self.ckpt8_shapes(T)[0][1]
+        _on_device(dev, "tp_row_bwd_ckpt8", stream, self._h, T, _use(dev, "dY", dY, (T, h), dt),
+                   _use_shards(dev, "W", W, p, (h, k), dt), *self._use_ckpt8(dev, T, Zq, Zs, H),
+                   _use_shards(dev, "dZ", dZ, p, (T, n1), dt), _use_shards(dev, "dW", dW, p, (h, k), dt),
+                   _use(dev, "dbias", dbias, (h,), torch.float32))
 
     def column_bwd(self, which, T, X, dZ, W, dW=None, dbias=None, dX_partials=None, stream=None):
         check(lib.tp_column_bwd(self._h, WHICH[which], T, _ptr(X), _arr(dZ), _arr(W), _arr(dW),
@@ -555,21 +542,20 @@ class Plan:
                                 dgate=None, post=None, dpost=None, pre=None, dpre=None, stream=None):
         """tp_gated_residual_norm_bwd: dx and df from dx_out and dy (either may be None), with
         dgate, dpost = (dgamma, dbeta) and dpre as fp32 sums over rows (each optional)."""
-        self._check_junction(kind, rows, (("f", f), ("x_out", x_out), ("dx_out", dx_out), ("dy", dy), ("dx", dx), ("df", df)),
-                             (("post", post), ("pre", pre)), gate, dgate, (("dpost", dpost), ("dpre", dpre)))
-        _want("stats", stats, (4, rows), torch.float32)
-        pg, pb = post if post else (None, None)
-        qg = pre[0] if pre else None
+        dev, dt, f32, h = dx.get_device(), self.torch_dtype, torch.float32, self.hidden
+        row = (rows, h)
+        gate_ptr, gate_rows, pg, pb, qg, _ = self._junction_weights(dev, kind, gate, post, pre)
         dpg, dpb = dpost if dpost else (None, None)
         dqg, dqb = dpre if dpre else (None, None)
         if kind == "rms":
             dpb = dqb = None
-        with _device_of(dx, f, x_out, stats, dx_out, dy, df, gate, dgate, pg, pb, qg, dpg, dpb, dqg, dqb):
-            check(lib.tp_gated_residual_norm_bwd(
-                self._h, NORMS[kind], rows, _ptr(f), _ptr(x_out), _ptr(stats), _ptr(dx_out), _ptr(dy), float(res_scale),
-                _ptr(gate), 0 if gate is None else gate.shape[0], _ptr(pg), _ptr(pb), _ptr(qg), _ptr(dx), _ptr(df),
-                _ptr(dgate), _ptr(dpg), _ptr(dpb), _ptr(dqg), _ptr(dqb), _stream(stream)),
-                "tp_gated_residual_norm_bwd")
+        _on_device(dev, "tp_gated_residual_norm_bwd", stream, self._h, NORMS[kind], rows, _use(dev, "f", f, row, dt),
+                   _use(dev, "x_out", x_out, row, dt), _use(dev, "stats", stats, (4, rows), f32),
+                   _use(dev, "dx_out", dx_out, row, dt), _use(dev, "dy", dy, row, dt), float(res_scale), gate_ptr,
+                   gate_rows, pg, pb, qg, _use(dev, "dx", dx, row, dt), _use(dev, "df", df, row, dt),
+                   _use(dev, "dgate", dgate, (gate_rows, h), f32), _use(dev, "dpost", dpg, (h,), f32),
+                   _use(dev, "dpost", dpb, (h,), f32), _use(dev, "dpre", dqg, (h,), f32),
+                   _use(dev, "dpre", dqb, (h,), f32))
 
     def attention_bwd(self, batch, seq, QKV, O, dO, LSE, dQKV, stream=None):
         check(lib.tp_attention_bwd(self._h, batch, seq, _arr(QKV), _arr(O), _arr(dO), _arr(LSE),

@@ -40,6 +40,8 @@ def test_loss_refusals(head):
     assert _loss(head, dW=(A + 48, A + 16)) == 1 and "alias" in tp.last_error()
     assert _loss(head, dW=(A + 48, A + 50)) == 3
     assert _loss(tp.Plan(64, 0, 0, 2, "bf16", "none")) == 1 and "vocab" in tp.last_error()
+    with pytest.raises(ValueError, match="set_vocab"):
+        tp.Plan(64, 0, 0, 2, "bf16", "none").vocab_linear_cross_entropy(0, torch.zeros(0, 64).bfloat16(), [], None, 1.0, None)
     assert tp.lib.tp_vocab_linear_cross_entropy(None, 4, A, _arr(A, A), A, 1.0, A, None, None, None, 0, None) == 1
     assert _loss(head, T=0) == 0  # no token, no gradient: nothing to do
 
@@ -159,3 +161,36 @@ def test_ckpt8_shapes_and_binding_checks():
         plan.column_fwd_ckpt8(5, X, W, None, [x.float() for x in q], s, H)
     with pytest.raises(ValueError, match="dZ"):
         plan.row_bwd_ckpt8(5, X, [torch.zeros(64, 1376).bfloat16()] * 2, q, s, H, H)
+
+
+def test_tensors_of_one_call_are_on_one_device(monkeypatch):
+    """With fakes of the device queries: a tensor on another device is refused, and the
+    tensors' device is made current for the call when it is not."""
+    seen, current = [], [0]
+
+    class Lib:
+        @staticmethod
+        def f(*args):
+            seen.append((current[-1], args))
+            return 0
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            current.append(self.d)
+
+        def __exit__(self, *e):
+            current.pop()
+
+    monkeypatch.setattr(tp, "lib", Lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    tp._on_device(1, "f", 5, "a")
+    tp._on_device(0, "f", 5, "b")
+    assert seen == [(1, ("a", 5)), (0, ("b", 5))]
+    with pytest.raises(ValueError, match="x: .* on cuda:1, got .* on cpu"):
+        tp._use(1, "x", torch.zeros(3), (3,), torch.float32)
+    with pytest.raises(ValueError, match=r"W\[0\]: .* on cuda:0, got .* on cpu"):
+        tp._use_shards(0, "W", [torch.zeros(3)], 1, (3,), torch.float32)
