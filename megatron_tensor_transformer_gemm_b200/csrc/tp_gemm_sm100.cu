@@ -22,6 +22,7 @@
 //   warp 1      TMEM allocator + single-thread tcgen05.mma issuer
 //   warps 2..9  epilogue: tcgen05.ld TMEM -> registers -> fused math -> HBM;
 //               two warps per TMEM lane quarter, each taking half of the columns
+//   warp 10     tile scheduler (see the tile ring)
 // The 128x256 fp32 accumulator lives in TMEM (256 columns); two accumulators
 // (all 512 columns) let the epilogue of one tile overlap the MMAs of the next.
 // Operands may be K-major or MN-major (the backward GEMMs read dY^T, X^T and
@@ -51,7 +52,8 @@ constexpr int BN = 256;
 constexpr int BK = 64;  // one 128-byte swizzle row of bf16
 constexpr int UMMA_K = 16;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kSchedWarp = 2 + kEpiWarps;
+constexpr int kThreads = 32 * (kSchedWarp + 1);
 constexpr int TMEM_COLS = 512;
 constexpr int kBarBytes = 512;  // barriers, TMEM slot, abort flag, tile ring
 constexpr int MN_BLOCK_BYTES = 64 * BK * 2;  // one 64-wide MN block of an MN-major tile
@@ -81,7 +83,7 @@ struct GroupArgs {
   int tile_begin;
   int num_kb;
   int nh;
-  int pad;
+  int tiles_m;
   void* D;
   int64_t ldd;
   void* D2;
@@ -126,6 +128,10 @@ struct alignas(64) GemmParams {
   int ksplit;
   int base_tiles;
   int kb_per_split;
+  // Tile order within a problem: bands of `band` tile rows, down each band's
+  // columns one after the other (1: row by row).
+  int band;
+  int ring_lag;  // see the tile ring
   int64_t split_stride;
   // Dynamic tile schedule: {draws, pairs done drawing}, zero at launch. Pair c
   // (or CTA c) starts on tile c; its leader then draws tile clusters + n with
@@ -167,8 +173,11 @@ __device__ __forceinline__ void decode_tile(const GemmParams& p, int t, int& g, 
   for (int i = 1; i < p.ngroups; ++i)
     if (t >= p.g[i].tile_begin) g = i;
   const int local = t - p.g[g].tile_begin;
-  mt = local / p.g[g].tiles_n;
-  nt = local - mt * p.g[g].tiles_n;
+  const int tiles_n = p.g[g].tiles_n;
+  const int b = local / (p.band * tiles_n), in_band = local - b * p.band * tiles_n;
+  const int rows = min(p.band, p.g[g].tiles_m - b * p.band);
+  nt = in_band / rows;
+  mt = b * p.band + in_band - nt * rows;
 }
 
 // K blocks of a tile: [kb0, kb0 + nkb) of its problem (the split's share
@@ -865,19 +874,31 @@ __device__ bool epilogue_tile_tma(const GemmParams& p, const GroupArgs& ga, int 
 // tiles in flight at any moment are a window of consecutive indices (the
 // operands they share stay in L2) and a CTA that drew narrow or short tiles
 // simply takes more: no pair waits at the end for one whose static share
-// held more work. The leader CTA's producer draws each tile and publishes it
-// through a ring of kRing slots in both CTAs of the pair; every consumer (the
-// MMA issuer, the epilogue warps, the peer's producer) reads each entry once
-// and arrives on the leader's `empty` barrier of that slot. -1 ends the list.
+// held more work. A warp of its own in the leader CTA draws each tile, decodes it
+// and publishes it through a ring of kRing slots in both CTAs of the pair; every
+// consumer (the MMA issuer, the producers, the epilogue warps) reads each entry
+// once and arrives on the leader's `empty` barrier of that slot. t = -1 ends the
+// list. Draws, divisions and the exchange so stay out of the producer's and the
+// issuer's way: with them there, a tile cost about 2 us beyond its MMAs (tiles of
+// 8 K blocks: 263 us for 8192 x 32000 x 512 without any epilogue).
+// Entry k is drawn once every consumer took entry k - lag. Two: the draw is one
+// tile ahead of the MMAs, so a CTA claims no tile long before it can begin it.
+// Tiles of few K blocks, of which the stages hold several, take more.
 constexpr int kRing = 8;
 struct TileRing {
-  volatile int* slot;
+  int4* slot;  // {t, g | ks << 8, mt, nt}
   uint64_t* full;
   uint64_t* empty;
+  int lag;
 };
-// Consumers of each entry: per CTA of the pair, the MMA issuer (leader) or
-// the producer (peer), plus the epilogue warps.
-constexpr int kRingConsumers = 1 + kEpiWarps;
+// Consumers of each entry: the leader's MMA issuer, and per CTA of the pair the
+// producer and the epilogue warps.
+template <int PAIR>
+constexpr int ring_consumers() { return 1 + PAIR * (1 + kEpiWarps); }
+
+struct Tile {
+  int t, g, mt, nt, ks;
+};
 
 // Called once by each leader that drew (a draw returned past the end, or it
 // gave up): the last of the pairs that draw sets the slot back to zero. Every
@@ -893,39 +914,49 @@ __device__ __forceinline__ void sched_done_drawing(const GemmParams& p, int clus
 }
 
 template <int PAIR>
-__device__ __forceinline__ bool ring_put(const TileRing& r, int k, int v, volatile int* abort,
+__device__ __forceinline__ bool ring_put(const TileRing& r, int k, const int4& v, volatile int* abort,
                                          unsigned* status) {
+  const int e = k - r.lag;  // lag <= kRing, so this also frees the slot
+  if (e >= 0 && !mbar_wait_cl(&r.empty[e % kRing], static_cast<uint32_t>(e / kRing) & 1u, abort, status)) return false;
   const int s = k % kRing;
-  const uint32_t par = static_cast<uint32_t>(k / kRing) & 1u;
-  if (!mbar_wait_cl(&r.empty[s], par ^ 1u, abort, status)) return false;
   r.slot[s] = v;
   if (PAIR == 2) {
-    st_shared_cluster_u32(map_shared(smem_u32(const_cast<int*>(&r.slot[s])), 1), static_cast<uint32_t>(v));
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(map_shared(smem_u32(&r.slot[s]), 1)),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
     mbar_arrive_cluster(map_shared(smem_u32(&r.full[s]), 1));
   }
   mbar_arrive_release_cluster(&r.full[s]);
   return true;
 }
-// One consumer thread: entry k (-2 when the wait gave up).
+__device__ __forceinline__ Tile ring_read(const TileRing& r, int s) {
+  int4 v;
+  asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(&r.slot[s]))
+               : "memory");
+  return Tile{v.x, v.y & 255, v.z, v.w, v.y >> 8};
+}
+// One consumer thread: entry k (t = -2 when the wait gave up).
 template <int PAIR>
-__device__ __forceinline__ int ring_take(const TileRing& r, int k, uint32_t rank, volatile int* abort,
-                                         unsigned* status) {
+__device__ __forceinline__ Tile ring_take(const TileRing& r, int k, uint32_t rank, volatile int* abort,
+                                          unsigned* status) {
   const int s = k % kRing;
   const uint32_t par = static_cast<uint32_t>(k / kRing) & 1u;
-  if (!mbar_wait_cl(&r.full[s], par, abort, status)) return -2;
-  const int v = r.slot[s];
+  if (!mbar_wait_cl(&r.full[s], par, abort, status)) return Tile{-2, 0, 0, 0, 0};
+  const Tile v = ring_read(r, s);
   if (PAIR == 2 && rank != 0) mbar_arrive_cluster(map_shared(smem_u32(&r.empty[s]), 0));
   else mbar_arrive_release_cluster(&r.empty[s]);
   return v;
 }
 // A whole warp: every lane reads entry k, lane 0 arrives once for the warp.
 template <int PAIR>
-__device__ __forceinline__ int ring_take_warp(const TileRing& r, int k, uint32_t rank, int lane,
-                                              volatile int* abort, unsigned* status) {
+__device__ __forceinline__ Tile ring_take_warp(const TileRing& r, int k, uint32_t rank, int lane,
+                                               volatile int* abort, unsigned* status) {
   const int s = k % kRing;
   const uint32_t par = static_cast<uint32_t>(k / kRing) & 1u;
-  if (!__all_sync(0xffffffffu, mbar_wait_cl(&r.full[s], par, abort, status))) return -2;
-  const int v = r.slot[s];
+  if (!__all_sync(0xffffffffu, mbar_wait_cl(&r.full[s], par, abort, status))) return Tile{-2, 0, 0, 0, 0};
+  const Tile v = ring_read(r, s);
   __syncwarp();
   if (lane == 0) {
     if (PAIR == 2 && rank != 0) mbar_arrive_cluster(map_shared(smem_u32(&r.empty[s]), 0));
@@ -955,8 +986,9 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
   TileRing ring;
   ring.full = drain + 2;
   ring.empty = ring.full + kRing;
-  ring.slot = reinterpret_cast<volatile int*>(ring.empty + kRing);
-  uint64_t* ebar = reinterpret_cast<uint64_t*>(const_cast<int*>(ring.slot) + kRing);  // [kEpiWarps]
+  uint64_t* ebar = ring.empty + kRing;  // [kEpiWarps]
+  ring.slot = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(ebar + kEpiWarps) + 15) & ~static_cast<uintptr_t>(15));
+  ring.lag = p.ring_lag;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -974,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     mbar_init(drain, 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(&ring.full[r], 1);
-      mbar_init(&ring.empty[r], PAIR * kRingConsumers);
+      mbar_init(&ring.empty[r], ring_consumers<PAIR>());
     }
     for (int w = 0; w < kEpiWarps; ++w) mbar_init(&ebar[w], 1);
     *abort_flag = 0;
@@ -1025,36 +1057,10 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) last_parity[s] = -1;
     bool ok = true;
-    int kseq = 0;
-    const int cluster = static_cast<int>(blockIdx.x) / PAIR, clusters = static_cast<int>(gridDim.x) / PAIR;
-    // The first tile needs no draw, so the first copies start at once; each
-    // draw is issued a tile ahead and its result first read one tile later.
-    int next = cluster;
-    bool drawing = false;  // a draw of this pair is outstanding or came back empty
-    bool done_drawing = !p.dyn_sched || cluster >= p.total_tiles;
-    for (;;) {
-      int t;
-      if (rank == 0) {  // draw the next tile and publish it (or the end)
-        t = next;
-        if (t < p.total_tiles) {
-          if (p.dyn_sched) {
-            next = clusters + static_cast<int>(atomicAdd(p.sched, 1u));
-            drawing = true;
-          } else {
-            next += clusters;
-          }
-        } else if (drawing && !done_drawing) {
-          sched_done_drawing(p, clusters);
-          done_drawing = true;
-        }
-        if (!ring_put<PAIR>(ring, kseq, t < p.total_tiles ? t : -1, abort_flag, p.status)) break;
-      } else {
-        t = ring_take<PAIR>(ring, kseq, rank, abort_flag, p.status);
-      }
-      ++kseq;
-      if (t < 0 || t >= p.total_tiles) break;
-      int g, mt, nt, ks;
-      decode_tile(p, t, g, mt, nt, ks);
+    for (int kseq = 0;; ++kseq) {
+      const Tile tile = ring_take<PAIR>(ring, kseq, rank, abort_flag, p.status);
+      if (tile.t < 0) break;
+      const int g = tile.g, mt = tile.mt, nt = tile.nt, ks = tile.ks;
       const GroupArgs& ga = p.g[g];
       int kb_first, kb_count;
       kb_range(p, ga, ks, kb_first, kb_count);
@@ -1131,9 +1137,6 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       }
       if (!ok) break;
     }
-    // A leader that left early (bounded wait gave up) still counts itself out,
-    // so the counters of this slot return to zero.
-    if (rank == 0 && !done_drawing) sched_done_drawing(p, clusters);
     // Drain: every copy of this CTA (and, for the leader, of the pair) has
     // landed before the CTA exits. The peer's copies complete on the leader's
     // barriers, which the leader drains.
@@ -1151,12 +1154,11 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int kseq = 0;; ++kseq) {
-      const int t = ring_take<PAIR>(ring, kseq, rank, abort_flag, p.status);
-      if (t < 0) break;
-      int g, mt, nt, ks;
-      decode_tile(p, t, g, mt, nt, ks);
+      const Tile tile = ring_take<PAIR>(ring, kseq, rank, abort_flag, p.status);
+      if (tile.t < 0) break;
+      const int g = tile.g, ks = tile.ks;
       const uint32_t idesc =
-          narrow_tile(p, p.g[g], nt * p.tile_n) ? idesc_narrow : idesc_full;
+          narrow_tile(p, p.g[g], tile.nt * p.tile_n) ? idesc_narrow : idesc_full;
       int kb_first, num_kb;
       kb_range(p, p.g[g], ks, kb_first, num_kb);
       if (p.kcat) {
@@ -1206,6 +1208,36 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     if (PAIR == 2) tc_commit_pair_mc(drain, 0x1);
     else tc_commit(drain);
     mbar_wait(drain, 0, abort_flag, p.status);
+  } else if (warp == kSchedWarp) {
+    // ------------------------------------------------------------ scheduler
+    if (lane == 0 && rank == 0) {
+      const int cluster = static_cast<int>(blockIdx.x) / PAIR, clusters = static_cast<int>(gridDim.x) / PAIR;
+      int next = cluster;  // the first tile needs no draw
+      bool drawing = false;
+      bool done_drawing = !p.dyn_sched || cluster >= p.total_tiles;
+      for (int k = 0;; ++k) {
+        const int t = next;
+        int4 v = make_int4(-1, 0, 0, 0);
+        if (t < p.total_tiles) {
+          if (p.dyn_sched) {
+            next = clusters + static_cast<int>(atomicAdd(p.sched, 1u));  // read in the next round
+            drawing = true;
+          } else {
+            next += clusters;
+          }
+          int g, mt, nt, ks;
+          decode_tile(p, t, g, mt, nt, ks);
+          v = make_int4(t, g | ks << 8, mt, nt);
+        } else if (drawing && !done_drawing) {
+          sched_done_drawing(p, clusters);
+          done_drawing = true;
+        }
+        if (!ring_put<PAIR>(ring, k, v, abort_flag, p.status) || v.x < 0) break;
+      }
+      // A leader that left early (bounded wait gave up) still counts itself out,
+      // so the counters of this slot return to zero.
+      if (!done_drawing) sched_done_drawing(p, clusters);
+    }
   } else if (warp >= 2) {
     // ------------------------------------------------------------- epilogue
     const int lg = warp & 3;          // TMEM lane quarter this warp may access
@@ -1216,10 +1248,9 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     EpiStage es{sE + (warp - 2) * kEpiBuf, &ebar[warp - 2], 0u, 0};
     bool ok = true;
     for (int kseq = 0;; ++kseq) {
-      const int t = ring_take_warp<PAIR>(ring, kseq, rank, lane, abort_flag, p.status);
-      if (t < 0) break;
-      int g, mt, nt, ks;
-      decode_tile(p, t, g, mt, nt, ks);
+      const Tile tile = ring_take_warp<PAIR>(ring, kseq, rank, lane, abort_flag, p.status);
+      if (tile.t < 0) break;
+      const int g = tile.g, mt = tile.mt, nt = tile.nt, ks = tile.ks;
       const GroupArgs& ga = p.g[g];
       const int row0 = mt * C::TILE_M + static_cast<int>(rank) * BM + lg * 32;
       const int n0 = nt * p.tile_n;
@@ -1633,6 +1664,7 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
       a.K = g.K;
       a.tiles_n = (o.N + tile_n - 1) / tile_n;
       a.tile_begin = tiles;
+      a.tiles_m = (o.M + tile_m - 1) / tile_m;
       a.num_kb = (g.K + BK - 1) / BK;
       a.nh = o.nh;
       a.D = o.D;
@@ -1721,6 +1753,26 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
     }
   }
   p.ngroups = nout;
+  // Bands of 8 tile rows when a sweep along one row of tiles reads more of B than
+  // stays in L2 (about half of its 126 MB): the 74 pairs then work on 8 rows and
+  // 9 columns of tiles, not on one row whose B panels come from HBM again for the
+  // next. 4096 x 131072 x 4096 over 8 shards (134 MB of B a shard): 5.13 -> 3.39 ms;
+  // 8192 x 57344 x 8192 (117 MB): 6.97 -> 6.17 ms. With B in L2 the orders are
+  // equal to within the clock's noise, and rows stay.
+  int64_t b_bytes = 0;
+  for (int i = 0; i < b.n; ++i)
+    b_bytes = b.kcat ? b_bytes + 2LL * b.g[0].N * b.g[i].K
+                     : std::max<int64_t>(b_bytes, 2LL * (swiglu ? 2 : 1) * b.g[i].N * b.g[i].K / ksplit);
+  p.band = b_bytes > 48LL * 1000 * 1000 ? 8 : 1;
+  int min_kb = 1 << 30;  // K blocks of the shortest tile
+  if (b.kcat) {
+    min_kb = 0;
+    for (int i = 0; i < b.n; ++i) min_kb += p.seg_kb[i];
+    min_kb /= ksplit;
+  } else {
+    for (int i = 0; i < nout; ++i) min_kb = std::min(min_kb, ksplit > 1 ? p.kb_per_split : p.g[i].num_kb);
+  }
+  p.ring_lag = min_kb >= 32 ? 2 : std::min(kRing, 2 + (Cfg<2>::STAGES + min_kb - 1) / std::max(1, min_kb));
   p.total_tiles = tiles;
   p.tile_n = tile_n;
   p.narrow_all = lay.narrow ? 1 : 0;
