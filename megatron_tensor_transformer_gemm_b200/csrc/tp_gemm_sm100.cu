@@ -631,85 +631,141 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
   }
 }
 
-// Cross-entropy epilogue (EPI_CE): a thread has one row and a half tile's
-// columns (a slot). A first pass over the accumulator takes their largest score,
-// a second the exponentials relative to it: their sum, and, when gradients
-// follow, the exponentials themselves in bf16: one rounding (2^-8) beside the
-// gradient's own, with fp32's range, so that an entry far below its slot's
-// largest keeps its gradient (fp16 would be 2^-11 but lose what is below 2^-25).
-// The scores exist only here, in fp32. Padding columns and the row's label take
-// no part (the label's score is added in full precision later).
-__device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uint32_t taddr, int row0, int n0, int half,
-                            bool narrow, int lane, EpiStage& es) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  const int cpw = narrow ? BN / 128 : BN / 64;  // 32-column chunks per slot
-  const int row = row0 + lane, col0 = g * ga.N;
-  const bool row_ok = row < ga.M;
-  const int limit = min(ga.N, p.ce_vocab - col0);                 // columns from here on are padding
-  const int label = row_ok ? p.ce_labels[row] - col0 : -1;        // in this problem's columns
-  float m = -INFINITY;
-#pragma unroll 1
-  for (int c = half * cpw; c < (half + 1) * cpw; ++c) {
-    const int j0 = n0 + c * 32;
-    if (j0 >= limit) break;  // warp-uniform
-    float v[32];
-    tmem_ld32(taddr + c * 32, v);
-    tc_wait_ld();
-    if (__any_sync(0xffffffffu, label >= j0 && label < j0 + 32) || j0 + 32 > limit) {
+// Cross-entropy epilogue (EPI_CE): a thread has one row and takes its columns 64
+// at a time (a slot), which it holds in registers: their largest score, the
+// exponentials relative to it, their sum, and, when gradients follow, the
+// exponentials themselves in bf16: one rounding (2^-8) beside the gradient's own,
+// with fp32's range, so that an entry far below its slot's largest keeps its
+// gradient (fp16 would be 2^-11 but lose what is below 2^-25). The scores exist
+// only here, in fp32. Padding columns and the row's label (`label`, as a column of
+// this problem) take no part: the label's score is added in full precision later.
+// Slots of 128 columns in two passes over TMEM, whose load latency they paid eight
+// times a tile, took about 8000 clocks a tile; K = 512 has 4096 of MMAs.
+__device__ __forceinline__ void ce_mask(float (&v)[32], int j0, int label, int limit) {
+  if (__any_sync(0xffffffffu, label >= j0 && label < j0 + 32) || j0 + 32 > limit) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) m = max3(m, v[i], v[i + 1]);
+    for (int i = 0; i < 32; ++i)
+      if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
   }
-  m *= kLog2e;
-  const float mo = m == -INFINITY ? 0.f : m;  // nothing left: every exp is 2^-inf = 0
-  float sum = 0.f;
+}
+__device__ __forceinline__ float ce_max(const float (&v)[32]) {
+  float m[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {  // four chains, not one of sixteen
+    m[q] = max3(v[8 * q], v[8 * q + 1], v[8 * q + 2]);
+    m[q] = max3(m[q], v[8 * q + 3], v[8 * q + 4]);
+    m[q] = max3(m[q], v[8 * q + 5], v[8 * q + 6]);
+    m[q] = fmaxf(m[q], v[8 * q + 7]);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// v -> packed exponentials (the first 16 words of v's bits); returns their sum.
+__device__ __forceinline__ float ce_exps(const float (&v)[32], float mo, uint32_t (&h)[16]) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float a = ex2(fmaf(v[i], kLog2e, -mo)), b = ex2(fmaf(v[i + 1], kLog2e, -mo));
+    s[(i / 2) & 3] += a + b;
+    h[i / 2] = pack_bf16x2(a, b);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+__device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uint32_t taddr, int row0, int n0, int half,
+                            bool narrow, int lane, int label, EpiStage& es) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int pairs = narrow ? 1 : 2;  // slots of this warp's half
+  const int row = row0 + lane;
+  const bool row_ok = row < ga.M;
+  const int limit = min(ga.N, p.ce_vocab - g * ga.N);  // columns from here on are padding
+  const uint32_t t0 = smem_u32(es.buf), t1 = t0 + kEpiTile;
 #pragma unroll 1
-  for (int c = half * cpw; c < (half + 1) * cpw; ++c) {
-    const int j0 = n0 + c * 32;
-    if (j0 >= ga.N) break;  // warp-uniform; padding columns are stored as zeros
-    float v[32];
-    tmem_ld32(taddr + c * 32, v);
+  for (int c = half * pairs; c < (half + 1) * pairs; ++c) {
+    const int j0 = n0 + c * 64;
+    if (j0 >= ga.N) break;  // warp-uniform
+    const bool two = j0 + 32 < ga.N;
+    float v[32], w[32];
+    tmem_ld32(taddr + c * 64, v);
+    tmem_ld32(taddr + c * 64 + 32, w);
     tc_wait_ld();
-    if (__any_sync(0xffffffffu, label >= j0 && label < j0 + 32) || j0 + 32 > limit) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
-    }
+    ce_mask(v, j0, label, limit);
+    ce_mask(w, j0 + 32, label, limit);
+    const float m = fmaxf(ce_max(v), ce_max(w)) * kLog2e;
+    const float mo = m == -INFINITY ? 0.f : m;  // nothing left: every exp is 2^-inf = 0
     uint32_t h[16];
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float a = ex2(fmaf(v[i], kLog2e, -mo)), b = ex2(fmaf(v[i + 1], kLog2e, -mo));
-      sum += a + b;
-      h[i / 2] = pack_bf16x2(a, b);
-    }
-    if (!ga.D) continue;
-    if (p.tma_epi) {
-      uint8_t* t = es.buf + es.slot * kEpiTile;
-      if (lane == 0) bulk_wait_read<1>();  // the store issued from this tile two chunks ago has read it
+    float sum = ce_exps(v, mo, h);
+    const bool store = ga.D != nullptr;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(ga.D) + static_cast<int64_t>(row) * ga.ldd + j0;
+    if (store && p.tma_epi) {
+      if (lane == 0) bulk_wait_read<0>();  // the last slot's stores have read both tiles
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        st_shared_v4(sw64(smem_u32(t), lane, q), make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(&p.tmE[g], t, j0, 0, row0);
-        bulk_commit();
-      }
-      es.slot ^= 1;
-    } else if (row_ok) {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(ga.D) + static_cast<int64_t>(row) * ga.ldd + j0;
+        st_shared_v4(sw64(t0, lane, q), make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
+    } else if (store && row_ok) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (j0 + q * 8 < ga.N)
           *reinterpret_cast<uint4*>(dst + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
     }
+    sum += ce_exps(w, mo, h);
+    if (store && p.tma_epi) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        st_shared_v4(sw64(t1, lane, q), make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmE[g], es.buf, j0, 0, row0);
+        if (two) tma_store_3d(&p.tmE[g], es.buf + kEpiTile, j0 + 32, 0, row0);
+        bulk_commit();
+      }
+    } else if (store && row_ok) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j0 + 32 + q * 8 < ga.N)
+          *reinterpret_cast<uint4*>(dst + 32 + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+    }
+    if (row_ok) p.ce_stats[row * p.ce_slots + static_cast<int64_t>(g) * ((ga.N + 63) / 64) + j0 / 64] = make_float2(m, sum);
   }
-  if (row_ok)
-    p.ce_stats[row * p.ce_slots + 2 * (static_cast<int64_t>(g) * ga.tiles_n + n0 / p.tile_n) + half] = make_float2(m, sum);
+}
+
+// Plain bf16 outputs without staged inputs, 64 columns at a time: both tiles of
+// the stage fill after one wait for TMEM and leave after one fence.
+__device__ void epilogue_store_tma(const GemmParams& p, const GroupArgs& ga, int gi, uint32_t taddr, int row0, int n0,
+                                   int half, bool narrow, int lane, EpiStage& es) {
+  const int pairs = narrow ? 1 : 2;
+  const uint32_t t0 = smem_u32(es.buf), t1 = t0 + kEpiTile;
+#pragma unroll 1
+  for (int c = half * pairs; c < (half + 1) * pairs; ++c) {
+    const int j0 = n0 + c * 64;
+    if (j0 >= ga.N) break;  // warp-uniform
+    const bool two = j0 + 32 < ga.N;
+    float v[32], w[32];
+    tmem_ld32(taddr + c * 64, v);
+    tmem_ld32(taddr + c * 64 + 32, w);
+    tc_wait_ld();
+    if (ga.bias) {
+      float b[32];
+      load_row_chunk_bf16(ga.bias, 0, 0, j0, ga.N, b);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += b[i];
+      load_row_chunk_bf16(ga.bias, 0, 0, j0 + 32, ga.N, b);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] += b[i];
+    }
+    if (lane == 0) bulk_wait_read<0>();  // the last stores have read both tiles
+    __syncwarp();
+    stage_write(t0, lane, v);
+    stage_write(t1, lane, w);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(&p.tmE[gi], es.buf, j0, 0, row0);
+      if (two) tma_store_3d(&p.tmE[gi], es.buf + kEpiTile, j0 + 32, 0, row0);
+      bulk_commit();
+    }
+  }
 }
 
 // Backward of an activation kept in 8 bits: dZ leaves through tmE, H through
@@ -1269,6 +1325,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const bool pre = p.tma_epi && tma_rows && epi_inputs(p, ga) > 0 &&
                        n0 + half * (narrow ? BN / 4 : BN / 2) < ga.N;
       if (pre && lane == 0) epi_issue_inputs(p, gi, epi_inputs(p, ga), n0 + half * (narrow ? BN / 4 : BN / 2), trow, es);
+      const int ce_label = p.epi == tpi::EPI_CE && row0 + lane < ga.M ? p.ce_labels[row0 + lane] - g * ga.N : -1;
       QGroup z0{}, z1{};
       const bool from_q = p.epi == tpi::EPI_DGELU_Q || p.epi == tpi::EPI_DSWIGLU_Q;
       if (from_q && p.tma_epi) {  // and so do its 8-bit groups
@@ -1290,11 +1347,13 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       if (p.tma_epi && !tma_rows) {
         // past the last row of a scattered launch: nothing to store
       } else if (p.epi == tpi::EPI_CE) {
-        epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, es);
+        epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, ce_label, es);
       } else if (p.tma_epi && (p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU)) {
         epilogue_fwd_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi && from_q) {
         epilogue_bwd_q_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es, z0, z1);
+      } else if (p.tma_epi && p.epi == tpi::EPI_STORE && epi_inputs(p, ga) == 0) {
+        epilogue_store_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi) {
         ok = epilogue_tile_tma(p, ga, gi, taddr, trow, n0, half, narrow, pre, lane, es, abort_flag, p.status);
       } else if (p.plain_staged) {
@@ -1784,7 +1843,7 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
     for (int i = 1; i < b.n; ++i)
       if (b.g[i].N != b.g[0].N) return fail(TP_ERR_ARG, "cross-entropy GEMM: problem %d has another width", i);
     if (b.kcat || b.scatter_n || ksplit > 1 || !b.ce_labels || !b.ce_stats ||
-        b.ce_slots < 2 * static_cast<int64_t>(b.n) * p.g[0].tiles_n)
+        b.ce_slots < static_cast<int64_t>(b.n) * ((b.g[0].N + 63) / 64))
       return fail(TP_ERR_ARG, "cross-entropy GEMM: statistics of %lld slots", static_cast<long long>(b.ce_slots));
     p.ce_vocab = b.ce_vocab;
     p.ce_labels = b.ce_labels;
@@ -1800,10 +1859,6 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   }
   if (pair == 2) return launch_kernel<2>(p, tiles, sms, st);
   return launch_kernel<1>(p, tiles, sms, st);
-}
-
-int gemm_tile_cols(const GemmBatch& b) {
-  return b.epi == EPI_SWIGLU || choose_layout(b, device_sms()).narrow ? BN / 2 : BN;
 }
 
 bool gemm_fills_gpu(const GemmBatch& b) {

@@ -284,11 +284,11 @@ struct GemmBatch {
   // buffers): the epilogue writes them with plain stores, never TMA.
   bool plain_stores;
   // EPI_CE: problem i's columns are vocab entries [i * N, (i + 1) * N), those
-  // from ce_vocab on padding. Each half of a tile's columns is a slot: for row r
-  // it writes ce_stats[r * ce_slots + slot] = (m, s), m the largest score times
-  // log2 e and s the sum of 2^(score log2 e - m) over its columns except padding
-  // and the row's label (both count as exp 0; m = -inf if none is left), and D
-  // (optional) those exps in bf16.
+  // from ce_vocab on padding. A slot is 64 columns of a problem (S = ceil(N / 64)
+  // of them): ce_stats[r * ce_slots + i * S + slot] = (m, s) for row r, m the
+  // largest score times log2 e and s the sum of 2^(score log2 e - m) over the
+  // slot's columns except padding and the row's label (both count as exp 0;
+  // m = -inf if none is left), and D (optional) holds those exps in bf16.
   int ce_vocab;
   const int32_t* ce_labels;
   float2* ce_stats;
@@ -302,10 +302,6 @@ struct GemmBatch {
 
 // bf16 tcgen05 tensor-core path (tp_gemm_sm100.cu).
 tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st);
-// Output columns per tile that a bf16 launch of b will use (256 or 128). Its
-// slots (EPI_CE): two per tile, each half of the columns the tile multiplies,
-// which are 256, or 128 where the launch or the tile (at most 128 left) is narrow.
-int gemm_tile_cols(const GemmBatch& b);
 // Whether a bf16 launch of b has at least as many tiles as CTA units (pairs or
 // CTAs) on this device, i.e. leaves no SM idle in its first wave.
 bool gemm_fills_gpu(const GemmBatch& b);

@@ -7,7 +7,7 @@
 //
 // Tokens are taken a chunk at a time. For bf16 plans the scores live only in the
 // tensor cores' fp32 accumulators: the GEMM's epilogue leaves, per row and slot of
-// 64 or 128 columns, their maximum m and sum of 2^(z log2 e - m), and, when
+// 64 columns, their maximum m and sum of 2^(z log2 e - m), and, when
 // gradients are wanted, the exponentials themselves in bf16 (relative to the slot's
 // maximum). A row kernel merges the slots (the running maximum and sum of a
 // softmax, joined), adds the label's score, and turns the exponentials into d in
@@ -102,12 +102,6 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
   }
 }
 
-// Where a shard's column lies in the statistics: see gemm_tile_cols.
-__device__ __forceinline__ int slot_of(int col, int Vs, int tile_cols) {
-  const int tile = col / tile_cols, n0 = tile * tile_cols;
-  return 2 * tile + (col - n0) / (Vs - n0 <= 128 || tile_cols == 128 ? 64 : 128);
-}
-
 // Merges a row's slot statistics, adds the label's score and writes loss and
 // lse; then (e != NULL) turns the row's exponentials into d in place.
 // The label's score is a dot product of its own, in fp32 by the CTA: the tensor
@@ -116,7 +110,7 @@ __device__ __forceinline__ int slot_of(int col, int Vs, int tile_cols) {
 // (few rows: the merge is short and repeated by each).
 constexpr int kFinThreads = 256;
 __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
-    const float2* stats, int slots, int tile_cols, int shard_slots, const __nv_bfloat16* X,
+    const float2* stats, int slots, int shard_slots, const __nv_bfloat16* X,
     const __grid_constant__ PtrArray W, int h, int vocab, int Vs, int p, const int32_t* labels, float scale, float* loss,
     float* lse_out, uint4* e, unsigned* status) {
   tpd::pdl_entry();
@@ -174,7 +168,7 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
   for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) {
     const uint4 u = row[i];
     const int sh = i / nv, c = (i - sh * nv) * 8;
-    const float m = st[sh * shard_slots + slot_of(c, Vs, tile_cols)].x;  // -inf: all its exps are 0
+    const float m = st[sh * shard_slots + c / 64].x;  // -inf: all its exps are 0
     const float f = tpd::ex2(m - lse2) * scale;
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     float d[8];
@@ -285,7 +279,7 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
   const int p = plan->p, h = plan->hidden, V = plan->vocab, Vp = plan->vocab_padded, Vs = Vp / p;
   constexpr size_t es = 2;
   const bool grad = dX || dW.p[0], dw = dW.p[0] != nullptr;
-  // without gradients, 8 bytes are kept per slot of at least 64 scores
+  // without gradients, 8 bytes are kept per slot of 64 scores
   const int64_t Tc = pick_chunk(T, Vp, h, grad ? 2.0 : 0.125, dw, chunk);
   const int64_t nch = (T + Tc - 1) / Tc;
 
@@ -351,14 +345,13 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.ce_labels = labels + t0;
     return b;
   };
-  // slots of a row at most (narrow tiles of 128 columns have two of 64)
-  const int64_t max_slots = 2LL * p * ((Vs + 127) / 128);
+  const int shard_slots = (Vs + 63) / 64, slots = p * shard_slots;  // see GemmBatch::ce_stats
 
   // scratch: d (from the exponentials or scores) | statistics | fp32 sums of dW | split-K partials
   const int sx = dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 1;
   const int sw = dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
   const size_t d_bytes = grad ? round256(static_cast<size_t>(Tc) * Vp * es) : 0;
-  const size_t st_bytes = round256(static_cast<size_t>(Tc) * max_slots * sizeof(float2));
+  const size_t st_bytes = round256(static_cast<size_t>(Tc) * slots * sizeof(float2));
   const size_t acc_bytes = dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
   const size_t part_bytes = std::max(sx > 1 ? static_cast<size_t>(sx) * Tc * h * 4 : 0, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
   void* ws = nullptr;
@@ -371,15 +364,13 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
   for (int64_t c = 0; c < nch; ++c) {
     const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
     GemmBatch b = score_batch(grad ? db : nullptr, t0, n);
-    const int tile = gemm_tile_cols(b);
-    const int shard_slots = 2 * ((Vs + tile - 1) / tile);
     b.ce_stats = stats;
-    b.ce_slots = static_cast<int64_t>(p) * shard_slots;
+    b.ce_slots = slots;
     TP_TRY(launch_gemm_bf16(b, st));
     // a few rows: enough CTAs a row to fill the GPU with the second part
     const int64_t parts = grad ? std::max<int64_t>(1, std::min<int64_t>(512 / n, Vp / 8 / kFinThreads)) : 1;
     (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
-                 stats, static_cast<int>(b.ce_slots), tile, shard_slots, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
+                 stats, slots, shard_slots, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
                  V, Vs, p, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
                  grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
     TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
