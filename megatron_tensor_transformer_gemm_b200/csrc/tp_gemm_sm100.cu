@@ -154,7 +154,7 @@ struct alignas(64) GemmParams {
   int ce_vocab;
   const int32_t* ce_labels;
   float2* ce_stats;
-  int64_t ce_slots;
+  int64_t ce_pairs;
   CUtensorMap tmE[TP_MAX_SHARDS];
   CUtensorMap tmX[TP_MAX_SHARDS];
   unsigned* status;
@@ -642,11 +642,9 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
 // Slots of 128 columns in two passes over TMEM, whose load latency they paid eight
 // times a tile, took about 8000 clocks a tile; K = 512 has 4096 of MMAs.
 __device__ __forceinline__ void ce_mask(float (&v)[32], int j0, int label, int limit) {
-  if (__any_sync(0xffffffffu, label >= j0 && label < j0 + 32) || j0 + 32 > limit) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
-  }
+  for (int i = 0; i < 32; ++i)
+    if (j0 + i == label || j0 + i >= limit) v[i] = -INFINITY;
 }
 __device__ __forceinline__ float ce_max(const float (&v)[32]) {
   float m[4];
@@ -671,14 +669,37 @@ __device__ __forceinline__ float ce_exps(const float (&v)[32], float mo, uint32_
   }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
+// A row's statistics of a tile, stored only once the next tile's accumulator is
+// ready (or at the end): the arrivals that hand the accumulator and the ring slot
+// back are releases, which would wait for stores just issued (a third of the
+// epilogue's time).
+struct CeStats {
+  float4* at;  // NULL: nothing waits
+  float4 v;
+  int slot;    // -1: both slots of the pair, else this one, in v.x and v.y
+  __device__ __forceinline__ void store() {
+    if (!at) return;
+    if (slot < 0) *at = v;
+    else reinterpret_cast<float2*>(at)[slot] = make_float2(v.x, v.y);
+    at = nullptr;
+  }
+};
 __device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uint32_t taddr, int row0, int n0, int half,
-                            bool narrow, int lane, int label, EpiStage& es) {
+                            bool narrow, int lane, int label, EpiStage& es, CeStats& out) {
   constexpr float kLog2e = 1.4426950408889634f;
   const int pairs = narrow ? 1 : 2;  // slots of this warp's half
   const int row = row0 + lane;
   const bool row_ok = row < ga.M;
   const int limit = min(ga.N, p.ce_vocab - g * ga.N);  // columns from here on are padding
   const uint32_t t0 = smem_u32(es.buf), t1 = t0 + kEpiTile;
+  const int first = n0 + half * pairs * 64, end = first + pairs * 64;  // this warp's columns
+  const bool mask = __any_sync(0xffffffffu, label >= first && label < end) || end > limit;
+  out.v = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  out.slot = narrow ? half : -1;
+  out.at = row_ok && first < ga.N
+               ? reinterpret_cast<float4*>(p.ce_stats) +
+                     row * p.ce_pairs + static_cast<int64_t>(g) * ((ga.N + 127) / 128) + first / 128
+               : nullptr;
 #pragma unroll 1
   for (int c = half * pairs; c < (half + 1) * pairs; ++c) {
     const int j0 = n0 + c * 64;
@@ -688,8 +709,10 @@ __device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uin
     tmem_ld32(taddr + c * 64, v);
     tmem_ld32(taddr + c * 64 + 32, w);
     tc_wait_ld();
-    ce_mask(v, j0, label, limit);
-    ce_mask(w, j0 + 32, label, limit);
+    if (mask) {
+      ce_mask(v, j0, label, limit);
+      ce_mask(w, j0 + 32, label, limit);
+    }
     const float m = fmaxf(ce_max(v), ce_max(w)) * kLog2e;
     const float mo = m == -INFINITY ? 0.f : m;  // nothing left: every exp is 2^-inf = 0
     uint32_t h[16];
@@ -726,7 +749,13 @@ __device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uin
         if (j0 + 32 + q * 8 < ga.N)
           *reinterpret_cast<uint4*>(dst + 32 + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
     }
-    if (row_ok) p.ce_stats[row * p.ce_slots + static_cast<int64_t>(g) * ((ga.N + 63) / 64) + j0 / 64] = make_float2(m, sum);
+    if (c == half * pairs) {
+      out.v.x = m;
+      out.v.y = sum;
+    } else {
+      out.v.z = m;
+      out.v.w = sum;
+    }
   }
 }
 
@@ -1302,6 +1331,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     uint32_t acc_phase = 0;
     const uint32_t tempty_leader = PAIR == 2 ? map_shared(smem_u32(&tempty[0]), 0) : 0u;
     EpiStage es{sE + (warp - 2) * kEpiBuf, &ebar[warp - 2], 0u, 0};
+    CeStats ce_out{};
     bool ok = true;
     for (int kseq = 0;; ++kseq) {
       const Tile tile = ring_take_warp<PAIR>(ring, kseq, rank, lane, abort_flag, p.status);
@@ -1342,12 +1372,13 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
         break;
       }
       tc_fence_after();
+      ce_out.store();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(lg * 32) << 16) +
                              static_cast<uint32_t>(acc * BN);
       if (p.tma_epi && !tma_rows) {
         // past the last row of a scattered launch: nothing to store
       } else if (p.epi == tpi::EPI_CE) {
-        epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, ce_label, es);
+        epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, ce_label, es, ce_out);
       } else if (p.tma_epi && (p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU)) {
         epilogue_fwd_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi && from_q) {
@@ -1371,6 +1402,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    ce_out.store();
     if (p.tma_epi && lane == 0) bulk_wait_all();  // every store of this warp has landed
   }
 
@@ -1842,13 +1874,12 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   if (b.epi == EPI_CE) {
     for (int i = 1; i < b.n; ++i)
       if (b.g[i].N != b.g[0].N) return fail(TP_ERR_ARG, "cross-entropy GEMM: problem %d has another width", i);
-    if (b.kcat || b.scatter_n || ksplit > 1 || !b.ce_labels || !b.ce_stats ||
-        b.ce_slots < static_cast<int64_t>(b.n) * ((b.g[0].N + 63) / 64))
-      return fail(TP_ERR_ARG, "cross-entropy GEMM: statistics of %lld slots", static_cast<long long>(b.ce_slots));
+    if (b.kcat || b.scatter_n || ksplit > 1 || !b.ce_labels || !b.ce_stats || b.ce_pairs < static_cast<int64_t>(b.n) * ((b.g[0].N + 127) / 128))
+      return fail(TP_ERR_ARG, "cross-entropy GEMM: statistics of %lld pairs of slots", static_cast<long long>(b.ce_pairs));
     p.ce_vocab = b.ce_vocab;
     p.ce_labels = b.ce_labels;
     p.ce_stats = b.ce_stats;
-    p.ce_slots = b.ce_slots;
+    p.ce_pairs = b.ce_pairs;
   }
   s = device_status_word(&p.status);
   if (s != TP_OK) return s;

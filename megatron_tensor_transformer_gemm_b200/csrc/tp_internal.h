@@ -284,15 +284,17 @@ struct GemmBatch {
   // buffers): the epilogue writes them with plain stores, never TMA.
   bool plain_stores;
   // EPI_CE: problem i's columns are vocab entries [i * N, (i + 1) * N), those
-  // from ce_vocab on padding. A slot is 64 columns of a problem (S = ceil(N / 64)
-  // of them): ce_stats[r * ce_slots + i * S + slot] = (m, s) for row r, m the
+  // from ce_vocab on padding. A slot is 64 columns of a problem, and a pair of
+  // slots (S = ceil(N / 128) pairs) has four floats per row: ce_stats[2 * (r *
+  // ce_pairs + i * S + pair) + slot] = (m, s) for row r (ce_pairs >= n S): m is the
   // largest score times log2 e and s the sum of 2^(score log2 e - m) over the
-  // slot's columns except padding and the row's label (both count as exp 0;
-  // m = -inf if none is left), and D (optional) holds those exps in bf16.
+  // slot's columns except padding and the row's label (both count as exp 0; m =
+  // -inf if none is left). A slot without columns may not be written. D (optional)
+  // holds those exps in bf16.
   int ce_vocab;
   const int32_t* ce_labels;
   float2* ce_stats;
-  int64_t ce_slots;
+  int64_t ce_pairs;
   // Split K (bf16 path, EPI_STORE, fp32 outputs, every problem with the same
   // K): ksplit > 1 runs each output tile ksplit times over consecutive K
   // ranges, split s writing its fp32 partial at g[i].D + s * split_stride.

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
 // (few rows: the merge is short and repeated by each).
 constexpr int kFinThreads = 256;
 __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
-    const float2* stats, int slots, int shard_slots, const __nv_bfloat16* X,
+    const float4* stats, int shard_pairs, const __nv_bfloat16* X,
     const __grid_constant__ PtrArray W, int h, int vocab, int Vs, int p, const int32_t* labels, float scale, float* loss,
     float* lse_out, uint4* e, unsigned* status) {
   tpd::pdl_entry();
@@ -136,9 +136,13 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
       }
     }
   }
-  const float2* st = stats + t * slots;
+  const float4* st = stats + t * p * shard_pairs;
   float2 acc = make_float2(-INFINITY, 0.f);
-  for (int i = threadIdx.x; i < slots; i += kFinThreads) acc = merge(acc, st[i]);
+  for (int i = threadIdx.x; i < p * shard_pairs; i += kFinThreads) {
+    const float4 v = st[i];
+    acc = merge(acc, make_float2(v.x, v.y));
+    if ((i % shard_pairs) * 128 + 64 < Vs) acc = merge(acc, make_float2(v.z, v.w));  // the pair's second slot has columns
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   if ((threadIdx.x & 31) == 0) dot[threadIdx.x >> 5] = z;
@@ -168,7 +172,8 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
   for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) {
     const uint4 u = row[i];
     const int sh = i / nv, c = (i - sh * nv) * 8;
-    const float m = st[sh * shard_slots + c / 64].x;  // -inf: all its exps are 0
+    const float4* at = st + sh * shard_pairs + c / 128;
+    const float m = c & 64 ? at->z : at->x;  // -inf: all its exps are 0
     const float f = tpd::ex2(m - lse2) * scale;
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     float d[8];
@@ -345,13 +350,13 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.ce_labels = labels + t0;
     return b;
   };
-  const int shard_slots = (Vs + 63) / 64, slots = p * shard_slots;  // see GemmBatch::ce_stats
+  const int shard_pairs = (Vs + 127) / 128;  // pairs of slots, see GemmBatch::ce_stats
 
   // scratch: d (from the exponentials or scores) | statistics | fp32 sums of dW | split-K partials
   const int sx = dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 1;
   const int sw = dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
   const size_t d_bytes = grad ? round256(static_cast<size_t>(Tc) * Vp * es) : 0;
-  const size_t st_bytes = round256(static_cast<size_t>(Tc) * slots * sizeof(float2));
+  const size_t st_bytes = round256(static_cast<size_t>(Tc) * p * shard_pairs * sizeof(float4));
   const size_t acc_bytes = dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
   const size_t part_bytes = std::max(sx > 1 ? static_cast<size_t>(sx) * Tc * h * 4 : 0, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
   void* ws = nullptr;
@@ -365,12 +370,12 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
     GemmBatch b = score_batch(grad ? db : nullptr, t0, n);
     b.ce_stats = stats;
-    b.ce_slots = slots;
+    b.ce_pairs = static_cast<int64_t>(p) * shard_pairs;
     TP_TRY(launch_gemm_bf16(b, st));
     // a few rows: enough CTAs a row to fill the GPU with the second part
     const int64_t parts = grad ? std::max<int64_t>(1, std::min<int64_t>(512 / n, Vp / 8 / kFinThreads)) : 1;
     (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
-                 stats, slots, shard_slots, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
+                 reinterpret_cast<const float4*>(stats), shard_pairs, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
                  V, Vs, p, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
                  grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
     TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
