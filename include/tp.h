@@ -523,7 +523,7 @@ TP_API tp_status tp_norm_sharded_bwd(tp_plan* plan, tp_norm_kind kind, int64_t r
  * LayerNorm). f is read with a post-norm or a gate, x_out with a pre-norm (NULL ok
  * otherwise; so is stats without any norm). The sums are deterministic. Uses the
  * plan's workspace: make a call of the same sizes before capturing one.
- * gate_rows <= 65534. With rows = 0 the sums are set to zero. */
+ * gate_rows <= 65536. With rows = 0 the sums are set to zero. */
 TP_API tp_status tp_gated_residual_norm_bwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, const void* f,
                                             const void* x_out, const float* stats, const void* dx_out,
                                             const void* dy, float res_scale, const void* gate,

@@ -1445,8 +1445,8 @@ tp_status tp_gated_residual_norm_bwd(tp_plan* plan, tp_norm_kind kind, int64_t r
   const bool layer = kind == TP_NORM_LAYER;
   if (!gamma_pre && dy) return fail(TP_ERR_ARG, "dy must be NULL without a pre-norm");
   if (!gate && dgate) return fail(TP_ERR_ARG, "dgate without a gate");
-  if (gate && gate_rows > 65534)
-    return fail(TP_ERR_UNSUPPORTED, "gate_rows = %lld exceeds 65534", static_cast<long long>(gate_rows));
+  if (gate && gate_rows > 65536)
+    return fail(TP_ERR_UNSUPPORTED, "gate_rows = %lld exceeds 65536", static_cast<long long>(gate_rows));
   if (!gamma_post && (dgamma_post || dbeta_post)) return fail(TP_ERR_ARG, "post-norm gradients without a post-norm");
   if (!gamma_pre && (dgamma_pre || dbeta_pre)) return fail(TP_ERR_ARG, "pre-norm gradients without a pre-norm");
   if (!layer && (dbeta_post || dbeta_pre)) return fail(TP_ERR_ARG, "RMSNorm has no beta gradient");

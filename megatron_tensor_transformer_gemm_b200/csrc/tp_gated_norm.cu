@@ -600,11 +600,10 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
   if (CL == 2) tpd::cluster_sync_all();  // neither CTA leaves while its peer may still write to it
 }
 
-// The column sums of the backward, each in a fixed order: a block owns 32
-// columns, eight lanes of four, and its kSumRows groups of eight lanes take CTAs
-// g, g + kSumRows, ...; the groups' sums are added in order. blockIdx.y = 0: the
-// norms' parameters (and a single gate row); blockIdx.y = b + 1: gate row b of
-// several.
+// The column sums of the backward, each in a fixed order. A block owns 32
+// columns, eight lanes of four. blockIdx.y = 0: the norms' parameters (and a single
+// gate row); its kSumRows groups of eight lanes take CTAs g, g + kSumRows, ... .
+// blockIdx.y = y: gate rows 4 (y - 1) ... of several, a quarter of the groups each.
 constexpr int kSumRows = 64;
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
   a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
@@ -617,7 +616,7 @@ __device__ __forceinline__ float4 four(const void* v, int64_t at) {
 template <typename T, bool RMS>
 __global__ void __launch_bounds__(8 * kSumRows) gated_norm_sums_kernel(const __grid_constant__ GatedNorm p, int64_t G) {
   tpd::pdl_entry();
-  __shared__ float4 red[kSumRows][8];
+  __shared__ float4 red[6][kSumRows / 4][8];
   const int group = threadIdx.x >> 3, lane = threadIdx.x & 7;  // group and its lane
   const int64_t col = (static_cast<int64_t>(blockIdx.x) * 8 + lane) * 4;
   const int64_t B = p.gate ? p.gate_rows : 1, per = p.rows / B;
@@ -626,12 +625,15 @@ __global__ void __launch_bounds__(8 * kSumRows) gated_norm_sums_kernel(const __g
   float4 v[6];  // P, Q, sum of g A, of g S, A, S
 #pragma unroll
   for (int i = 0; i < 6; ++i) v[i] = zero;
+  constexpr int kQuarter = kSumRows / 4;
+  const int64_t gate_row = all ? 0 : (blockIdx.y - 1) * 4 + group / kQuarter;
+  const bool mine = gate_row < B;
   int64_t c0 = 0, c1 = G;
-  if (!all) {
-    c0 = range_of(p.rows, G, (blockIdx.y - 1) * per);
-    c1 = range_of(p.rows, G, blockIdx.y * per - 1) + 1;
+  if (!all && mine) {
+    c0 = range_of(p.rows, G, gate_row * per);
+    c1 = range_of(p.rows, G, (gate_row + 1) * per - 1) + 1;
   }
-  if (in) {
+  if (in && mine) {
     if (all && p.pre_g) {
 #pragma unroll 4
       for (int64_t c = group; c < G; c += kSumRows) {
@@ -641,41 +643,85 @@ __global__ void __launch_bounds__(8 * kSumRows) gated_norm_sums_kernel(const __g
       }
     }
     if (use_f && (!all || B == 1)) {
-      const int64_t b = all ? 0 : blockIdx.y - 1;
+      const int first = all ? group : group % kQuarter, step = all ? kSumRows : kQuarter;
 #pragma unroll 4
-      for (int64_t c = c0 + group; c < c1; c += kSumRows) {
-        const float* s = p.seg + (c + b) * 2 * p.h + col;
+      for (int64_t c = c0 + first; c < c1; c += step) {
+        const float* s = p.seg + (c + gate_row) * 2 * p.h + col;
         add4(v[4], *reinterpret_cast<const float4*>(s));
         if (!RMS) add4(v[5], *reinterpret_cast<const float4*>(s + p.h));
       }
-    } else if (use_f && p.dpost_g) {  // several gate rows, weighted
-      for (int64_t c = group; c < G; c += kSumRows) {
-        const int2 r = p.runs[c];
-        for (int b = r.x; b <= r.y; ++b) {
-          const float* s = p.seg + (c + b) * 2 * p.h + col;
-          const float4 A = *reinterpret_cast<const float4*>(s), g = four<T>(p.gate, b * p.h + col);
-          v[2].x = fmaf(g.x, A.x, v[2].x); v[2].y = fmaf(g.y, A.y, v[2].y);
-          v[2].z = fmaf(g.z, A.z, v[2].z); v[2].w = fmaf(g.w, A.w, v[2].w);
-          if (!RMS) {
-            const float4 S = *reinterpret_cast<const float4*>(s + p.h);
-            v[3].x = fmaf(g.x, S.x, v[3].x); v[3].y = fmaf(g.y, S.y, v[3].y);
-            v[3].z = fmaf(g.z, S.z, v[3].z); v[3].w = fmaf(g.w, S.w, v[3].w);
+    } else if (use_f && (p.dpost_g || p.dpost_b)) {  // several gate rows, weighted
+      auto add = [&](const float4& A, const float4& S, const float4& g) {
+        v[2].x = fmaf(g.x, A.x, v[2].x); v[2].y = fmaf(g.y, A.y, v[2].y);
+        v[2].z = fmaf(g.z, A.z, v[2].z); v[2].w = fmaf(g.w, A.w, v[2].w);
+        if (!RMS) {
+          v[3].x = fmaf(g.x, S.x, v[3].x); v[3].y = fmaf(g.y, S.y, v[3].y);
+          v[3].z = fmaf(g.z, S.z, v[3].z); v[3].w = fmaf(g.w, S.w, v[3].w);
+        }
+      };
+      auto load = [&](int64_t c, int b, float4& A, float4& S, float4& g) {
+        const float* s = p.seg + (c + b) * 2 * p.h + col;
+        A = *reinterpret_cast<const float4*>(s);
+        if (!RMS) S = *reinterpret_cast<const float4*>(s + p.h);
+        g = four<T>(p.gate, static_cast<int64_t>(b) * p.h + col);
+      };
+      constexpr int U = 4;  // CTAs whose loads are in flight together
+      for (int64_t c0 = group; c0 < G; c0 += U * kSumRows) {
+        int2 r[U];
+        float4 A[U], S[U], g[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          r[u] = c0 + u * kSumRows < G ? p.runs[c0 + u * kSumRows] : make_int2(0, -1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          A[u] = S[u] = g[u] = zero;
+          if (r[u].y >= 0) load(c0 + u * kSumRows, r[u].x, A[u], S[u], g[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          add(A[u], S[u], g[u]);
+          for (int b = r[u].x + 1; b <= r[u].y; ++b) {  // a CTA whose rows pass into further gate rows
+            load(c0 + u * kSumRows, b, A[u], S[u], g[u]);
+            add(A[u], S[u], g[u]);
           }
         }
       }
     }
   }
+  // the four groups of a warp, then the warps, in order
 #pragma unroll
   for (int i = 0; i < 6; ++i) {
     if (RMS && (i & 1)) continue;
-    red[group][lane] = v[i];
-    __syncthreads();
-    if (group == 0)
-#pragma unroll 8
-      for (int w = 1; w < kSumRows; ++w) add4(v[i], red[w][lane]);
-    __syncthreads();
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1)
+      add4(v[i], make_float4(__shfl_xor_sync(0xffffffffu, v[i].x, o), __shfl_xor_sync(0xffffffffu, v[i].y, o),
+                             __shfl_xor_sync(0xffffffffu, v[i].z, o), __shfl_xor_sync(0xffffffffu, v[i].w, o)));
+    if ((threadIdx.x & 31) < 8) red[i][threadIdx.x >> 5][lane] = v[i];
   }
-  if (group != 0 || !in) return;
+  __syncthreads();
+  constexpr int kWarps = kSumRows / 4;
+  if (all) {  // group i adds the warps' sums of v[i]
+    if (group < 6 && !(RMS && (group & 1))) {
+      float4 t = red[group][0][lane];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) add4(t, red[group][w][lane]);
+      red[group][0][lane] = t;
+    }
+    __syncthreads();
+    if (group != 0 || !in) return;
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+      if (!(RMS && (i & 1))) v[i] = red[i][0][lane];
+  } else {  // the first group of each quarter, its gate row's two sums
+    if (group % kQuarter != 0 || !in || !mine) return;
+#pragma unroll
+    for (int i = 4; i < 6; ++i) {
+      if (RMS && (i & 1)) continue;
+      v[i] = red[i][group / 4][lane];
+#pragma unroll
+      for (int w = 1; w < kWarps / 4; ++w) add4(v[i], red[i][group / 4 + w][lane]);
+    }
+  }
   if (all && B == 1 && use_f) {  // one gate row: its weight once, after the sum
     const float4 g = p.gate ? four<T>(p.gate, col) : make_float4(1.f, 1.f, 1.f, 1.f);
     v[2] = make_float4(g.x * v[4].x, g.y * v[4].y, g.z * v[4].z, g.w * v[4].w);
@@ -695,7 +741,7 @@ __global__ void __launch_bounds__(8 * kSumRows) gated_norm_sums_kernel(const __g
   if (p.dgate && (all ? B == 1 : true)) {
     const float4 g = p.post_g ? four<T>(p.post_g, col) : make_float4(1.f, 1.f, 1.f, 1.f);
     const float4 b = p.post_g && !RMS ? four<T>(p.post_b, col) : zero;
-    put(p.dgate + (all ? 0 : (blockIdx.y - 1) * p.h),
+    put(p.dgate + gate_row * p.h,
         make_float4(g.x * v[4].x + b.x * v[5].x, g.y * v[4].y + b.y * v[5].y, g.z * v[4].z + b.z * v[5].z,
                     g.w * v[4].w + b.w * v[5].w));
   }
@@ -764,7 +810,7 @@ tp_status launch_bwd(tp_plan* plan, GatedNorm p, cudaStream_t st) {
   TP_TRY(tpi::cuda_status(cudaLaunchKernelEx(&cfg, kernel, p, G, narr, vec_cta, status), "gated_residual_norm_bwd"));
   TP_TRY(tpi::after_launch("gated_residual_norm_bwd"));
   if (!(p.dgate || p.dpost_g || p.dpost_b || p.dpre_g || p.dpre_b)) return TP_OK;
-  const dim3 g2(static_cast<unsigned>((p.h + 31) / 32), p.dgate && B > 1 ? static_cast<unsigned>(B + 1) : 1u);
+  const dim3 g2(static_cast<unsigned>((p.h + 31) / 32), p.dgate && B > 1 ? static_cast<unsigned>((B + 3) / 4 + 1) : 1u);
   (void)tpi::launch(gated_norm_sums_kernel<T, RMS>, g2, dim3(8 * kSumRows), 0, st, p, G);
   return tpi::after_launch("gated_residual_norm_bwd/sums");
 }

@@ -223,6 +223,27 @@ def test_backward_with_parts_missing(which):
         assert float(out["dpre"][0].abs().max()) == 0 and float(out["dpre"][1].abs().max()) == 0
 
 
+@pytest.mark.parametrize("B", [1, 3])
+def test_each_sum_alone(B):
+    """Any one of the sums can be asked for without the others, with the same bits."""
+    tp = _tp()
+    d, dt = _inputs(96, 264, "bf16", B, True, True, seed=14)
+    plan = tp.Plan(264, 0, 0, 1, "bf16", "none")
+    x_out, stats = _saved(d, "layer", 1.0, dt)
+    xo, st, args = dev(x_out), dev(stats), {k: _d(v) for k, v in d.items()}
+    full = _backward(plan, "layer", 96, d, xo, st, 1.0)
+    want = {"dgate": full["dgate"], "dpost0": full["dpost"][0], "dpost1": full["dpost"][1], "dpre0": full["dpre"][0],
+            "dpre1": full["dpre"][1]}
+    for name, ref in want.items():
+        got = torch.full_like(ref, 7.0)
+        pair = lambda k: ((got, None) if name == k + "0" else (None, got) if name == k + "1" else None)  # noqa: E731
+        dx, df = torch.empty_like(xo), torch.empty_like(xo)
+        plan.gated_residual_norm_bwd("layer", 96, args["f"], xo, st, args["dx_out"], args["dy"], dx, df, gate=args["gate"],
+                                     dgate=got if name == "dgate" else None, post=args["post"], dpost=pair("dpost"),
+                                     pre=args["pre"], dpre=pair("dpre"))
+        assert torch.equal(got, ref) and torch.equal(dx, full["dx"]) and torch.equal(df, full["df"]), name
+
+
 def test_in_place_and_zero_rows():
     tp = _tp()
     d, dt = _inputs(50, 1024, "bf16", 1, True, True, seed=5)

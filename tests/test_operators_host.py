@@ -96,7 +96,7 @@ def test_gated_norm_refusals():
     assert _bwd(plan, kind=1, dpb=A) == 1 and "RMSNorm" in tp.last_error()
     assert _bwd(plan, f=None) == 1 and _bwd(plan, xo=None) == 1 and _bwd(plan, stats=None) == 1
     assert _bwd(plan, dx=None) == 1 and _bwd(plan, df=A + 16) == 1 and "alias" in tp.last_error()
-    assert _bwd(plan, rows=131072, gate=A, gate_rows=65536) == 5
+    assert _bwd(plan, rows=131074, gate=A, gate_rows=65537) == 5
     assert _bwd(plan, dqg=A + 4) == 3
     assert _bwd(plan, rows=0, f=None, xo=None, stats=None, dxo=None, dy=None, dx=None, df=None) == 0
 
