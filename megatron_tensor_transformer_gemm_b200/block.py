@@ -13,6 +13,11 @@ reduce / reduce-scatter / all-gather kernels.
              heads -> out-projection partials -> reduce (+bias, +residual), and
              its backward.                         (TP walkthrough §3.1)
   TPLayer    pre-LN layer: x1 = x + Attn(LN1(x)); y = x1 + MLP(LN2(x1)).
+  TPGatedLayer  layer whose sublayers meet in gated, scaled residual junctions with a
+             norm after and before each (tp_gated_residual_norm_*), its MLP's
+             pre-activations kept in 8 bits.
+  TPHead     vocab-sharded output head with its cross-entropy, without the logits
+             (tp_vocab_linear_cross_entropy).      (TP walkthrough §6.2)
   SPMLP      Megatron-SP: LN on sequence shards fused with the all-gather ->
              column -> row -> reduce-scatter; backward: all-gather of dY ->
              row bwd -> column bwd -> reduce-scatter of dX partials -> LN bwd
@@ -34,7 +39,7 @@ class TPMLP:
 
     def __init__(self, hidden: int, ffn: int, p: int, act: str = "gelu", dtype: str = "bf16",
                  device="cuda", bias: bool = False, fused: bool = False, overlap_chunks: int = 0,
-                 group_wgrad: bool = False):
+                 group_wgrad: bool = False, ckpt8: bool = False, H_scratch=None):
         """fused: sum the shards inside the row GEMM and the column-backward dX
         GEMM (tp_row_fwd_reduce / tp_column_bwd_reduce) instead of writing p
         partials and reducing them (tp_row_fwd_partial + tp_reduce_partials).
@@ -44,7 +49,13 @@ class TPMLP:
         Parallel" §三, with the local reduce in place of the collective).
         group_wgrad: the row and column backward's weight gradients run as one
         grouped launch (tp_set_wgrad_grouping; backward() issues both). Off by
-        default: on the 7B step it measured slower than two launches."""
+        default: on the 7B step it measured slower than two launches.
+        ckpt8: keep the pre-activation for the backward as 8-bit codes and scales
+        (tp_column_fwd_ckpt8) and compute the activation again there, so that
+        between the passes the MLP holds 1.03 bytes per pre-activation element in
+        place of the 2 of Z and the 2 of H. H is then scratch within a pass:
+        H_scratch (a list of p [T, ffn/p] tensors) lets layers share it."""
+        self.ckpt8, self._H_scratch = ckpt8, H_scratch
         self.h, self.f, self.p, self.act = hidden, ffn, p, act
         self.fused = fused
         self.chunks = overlap_chunks if (overlap_chunks > 1 and not fused) else 0
@@ -80,8 +91,13 @@ class TPMLP:
             return
         dev, dt, p = self.device, self.dt, self.p
         self._T = T
-        self.Z = [_empty((T, self.n1), dt, dev) for _ in range(p)]
-        self.H = [_empty((T, self.fp), dt, dev) for _ in range(p)]
+        if self.ckpt8:
+            codes, scales = self.plan.ckpt8_shapes(T)
+            self.Zq = [_empty(codes, torch.float8_e4m3fn, dev) for _ in range(p)]
+            self.Zs = [_empty(scales, torch.uint8, dev) for _ in range(p)]
+        else:
+            self.Z = [_empty((T, self.n1), dt, dev) for _ in range(p)]
+        self.H = self._H_scratch or [_empty((T, self.fp), dt, dev) for _ in range(p)]
         self.P = None if self.fused else [_empty((T, self.h), dt, dev) for _ in range(p)]
         self.Y = _empty((T, self.h), dt, dev)
         if backward:
@@ -99,7 +115,10 @@ class TPMLP:
         self.alloc(T, backward=hasattr(self, "dZ") or True)
         self.X = X
         pl = self.plan
-        pl.column_fwd("mlp", T, X, self.W1, self.b1, self.Z if self.act != "none" else None, self.H)
+        if self.ckpt8:
+            pl.column_fwd_ckpt8(T, X, self.W1, self.b1, self.Zq, self.Zs, self.H)
+        else:
+            pl.column_fwd("mlp", T, X, self.W1, self.b1, self.Z if self.act != "none" else None, self.H)
         Y = self.Y if out is None else out
         if self.fused:
             pl.row_fwd_reduce("mlp", T, self.H, self.W2, self.b2, residual, Y)
@@ -145,8 +164,11 @@ class TPMLP:
     def backward(self, dY: torch.Tensor, out=None):
         T = dY.shape[0]
         pl = self.plan
-        pl.row_bwd("mlp", T, dY, self.H, self.W2, self.Z if self.act != "none" else None, self.dZ,
-                   self.dW2, self.db2)
+        if self.ckpt8:
+            pl.row_bwd_ckpt8(T, dY, self.W2, self.Zq, self.Zs, self.H, self.dZ, self.dW2, self.db2)
+        else:
+            pl.row_bwd("mlp", T, dY, self.H, self.W2, self.Z if self.act != "none" else None, self.dZ,
+                       self.dW2, self.db2)
         dX = self.dX if out is None else out
         if self.fused:
             pl.column_bwd_reduce("mlp", T, self.X, self.dZ, self.W1, self.dW1, self.db1, dX)
@@ -471,6 +493,110 @@ class TPLayer:
         if join:
             backward_join()
         return self.dx
+
+
+class TPGatedLayer:
+    """Transformer layer whose sublayers meet in gated residual junctions, split over p
+    shards on one GPU. With x the residual stream and u its norm (the layer's inputs):
+
+      a = Attn(u);  x1 = s x + g1 Norm(a);  u1 = Norm(x1)      one junction call
+      m = MLP(u1);  x2 = s x1 + g2 Norm(m); u2 = Norm(x2)      and another
+
+    (x2, u2) are the next layer's (x, u); the last layer's u2 goes to the output head.
+    gate_rows: rows of each gate (1: per channel; batch: per sequence; 0: none)."""
+
+    def __init__(self, hidden: int, ffn: int, heads: int, p: int, act: str = "swiglu", norm: str = "rms",
+                 res_scale: float = 1.0, gate_rows: int = 1, device="cuda", ckpt8: bool = True, H_scratch=None):
+        self.h, self.norm, self.rs = hidden, norm, res_scale
+        self.device = torch.device(device)
+        self.attn = TPAttention(hidden, heads, p, device, fused=True)
+        self.mlp = TPMLP(hidden, ffn, p, act, "bf16", device, fused=True, ckpt8=ckpt8, H_scratch=H_scratch)
+        self.plan = Plan(hidden, 0, 0, 1, "bf16", "none")  # the junctions
+        bf = dict(dtype=torch.bfloat16, device=self.device)
+        pair = lambda: (torch.ones(hidden, **bf), torch.zeros(hidden, **bf))  # noqa: E731
+        self.post, self.pre = [pair(), pair()], [pair(), pair()]
+        self.gate = [torch.ones(gate_rows, hidden, **bf) if gate_rows else None for _ in range(2)]
+        self._T = None
+
+    def alloc(self, T: int):
+        if self._T == T:
+            return
+        self._T = T
+        dev, h = self.device, self.h
+        bf = lambda: _empty((T, h), torch.bfloat16, dev)  # noqa: E731
+        f32 = lambda *s: _empty(s, torch.float32, dev)  # noqa: E731
+        self.a, self.m = bf(), bf()
+        self.xs, self.us = [bf(), bf()], [bf(), bf()]
+        self.stats = [f32(4, T), f32(4, T)]
+        self.da, self.dm, self.dx1, self.dx = bf(), bf(), bf(), bf()
+        self.dgate = [f32(*g.shape) if g is not None else None for g in self.gate]
+        beta = self.norm == "layer"
+        self.dpost = [(f32(h), f32(h) if beta else None) for _ in range(2)]
+        self.dpre = [(f32(h), f32(h) if beta else None) for _ in range(2)]
+
+    def _junction(self, k, T, x, f):
+        self.plan.gated_residual_norm_fwd(self.norm, T, x, f, self.xs[k], self.us[k], res_scale=self.rs,
+                                          gate=self.gate[k], post=self.post[k], pre=self.pre[k], stats=self.stats[k])
+        return self.xs[k], self.us[k]
+
+    def _junction_bwd(self, k, T, f, dx_out, dy, dx, df):
+        self.plan.gated_residual_norm_bwd(self.norm, T, f, self.xs[k], self.stats[k], dx_out, dy, dx, df,
+                                          res_scale=self.rs, gate=self.gate[k], dgate=self.dgate[k], post=self.post[k],
+                                          dpost=self.dpost[k], pre=self.pre[k], dpre=self.dpre[k])
+
+    def forward(self, x: torch.Tensor, u: torch.Tensor, batch: int, seq: int):
+        T = batch * seq
+        self.alloc(T)
+        self.attn.forward(u, batch, seq, out=self.a)
+        x1, u1 = self._junction(0, T, x, self.a)
+        self.mlp.forward(u1, out=self.m)
+        return self._junction(1, T, x1, self.m)
+
+    def backward(self, dx2, du2, batch: int, seq: int):
+        """Gradients (dx, du) of the layer's inputs from those of its outputs (either may be None)."""
+        T = batch * seq
+        self._junction_bwd(1, T, self.m, dx2, du2, self.dx1, self.dm)
+        du1 = self.mlp.backward(self.dm)
+        self._junction_bwd(0, T, self.a, self.dx1, du1, self.dx, self.da)
+        return self.dx, self.attn.backward(self.da, batch, seq)
+
+
+class TPHead:
+    """Output head split by vocab rows over p shards on one GPU, with its softmax
+    cross-entropy in one call: loss, the hidden states' gradient and the weight's,
+    without the logits."""
+
+    def __init__(self, hidden: int, vocab: int, p: int, dtype: str = "bf16", device="cuda"):
+        self.plan = Plan(hidden, 0, 0, p, dtype, "none")
+        self.vocab_padded = self.plan.set_vocab(vocab)
+        self.device, self.dt = torch.device(device), self.plan.torch_dtype
+        self.W = [torch.zeros(self.vocab_padded // p, hidden, dtype=self.dt, device=self.device) for _ in range(p)]
+        self._T = None
+
+    def load_weight(self, W_full: torch.Tensor):
+        """Shard a [vocab, hidden] (or padded) weight already on the device."""
+        full = torch.zeros(self.vocab_padded, W_full.shape[1], dtype=self.dt, device=self.device)
+        full[:W_full.shape[0]] = W_full
+        self.plan.shard_column("vocab", full, self.W)
+
+    def alloc(self, T: int, backward: bool = True):
+        if self._T != T:
+            self._T = T
+            self.loss_rows, self.lse = (_empty((T,), torch.float32, self.device) for _ in range(2))
+            self.dX = self.dW = None
+        if backward and self.dX is None:
+            self.dX = _empty((T, self.W[0].shape[1]), self.dt, self.device)
+            self.dW = [torch.empty_like(w) for w in self.W]
+
+    def loss(self, X: torch.Tensor, labels: torch.Tensor, grad_scale: float | None = None, chunk: int = 0):
+        """Loss of every token (0 where its label is negative). With grad_scale, self.dX and
+        self.dW receive the gradients of grad_scale times the losses' sum."""
+        T = X.shape[0]
+        grad = grad_scale is not None
+        self.alloc(T, grad)
+        self.plan.vocab_linear_cross_entropy(T, X, self.W, labels, grad_scale if grad else 1.0, self.loss_rows, self.lse,
+                                             self.dX if grad else None, self.dW if grad else None, chunk)
+        return self.loss_rows
 
 
 class CapturedStep:
