@@ -443,7 +443,8 @@ TP_API tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void
  * H[i] [T, ffn/p] = the activation of the decoded Z (NULL array skips when dW is
  * NULL), dW[i] = dY^T H[i] with that H, and dbias. Everything runs on `stream`
  * (the deferred and grouped modes do not apply; a waiting weight gradient is
- * launched first). With T = 0, dW and dbias are set to zero. */
+ * launched first). Uses the plan's workspace: make a call of the same sizes before
+ * capturing one. With T = 0, dW and dbias are set to zero. */
 TP_API tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void* const* W,
                                   const void* const* Zq, const uint8_t* const* Zs, void* const* H,
                                   void* const* dZ, void* const* dW, float* dbias, void* stream);

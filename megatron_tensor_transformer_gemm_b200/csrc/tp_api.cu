@@ -1892,14 +1892,14 @@ tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void*
       o.ldd = k;
     }
   }
+  // the workspace first: a call that a capture refuses has launched nothing
+  const int s = dW ? gemm_split_k(w) : 1;
+  void* part = nullptr;
+  if (s > 1) TP_TRY(scratch(plan, static_cast<size_t>(s) * p * h * k * sizeof(float), st, &part));
   TP_TRY(launch_gemm_bf16(b, st));
   if (dbias) TP_TRY(launch_column_sum(plan, dY, T, h, h, dbias, 0, plan->dtype, st));
   if (!dW) return TP_OK;
-  const int s = gemm_split_k(w);
-  if (s <= 1) return launch_gemm_bf16(w, st);
-  void* part = nullptr;
-  TP_TRY(scratch(plan, static_cast<size_t>(s) * p * h * k * sizeof(float), st, &part));
-  return launch_gemm_split(w, s, static_cast<float*>(part), st);
+  return s > 1 ? launch_gemm_split(w, s, static_cast<float*>(part), st) : launch_gemm_bf16(w, st);
 }
 
 tp_status tp_column_bwd(tp_plan* plan, tp_which which, int64_t T, const void* X,

@@ -10,6 +10,8 @@
 //   EPI_DSWIGLU    dZ = [acc*u*SiLU'(g) | acc*SiLU(g)]   row layer backward
 //   EPI_DGELU_Q / EPI_DSWIGLU_Q: the same from Z kept in 8 bits (which
 //   EPI_BIAS_GELU / EPI_SWIGLU may write instead of Z), with H computed again
+//   EPI_CE         per row and 64 columns the maximum and sum of a softmax, and the
+//                  exponentials (optional)               output head with its loss
 // (TP walkthrough 2kiu.com §2.1-§2.2 and §3.2; 张量并行 wiki, 两种切法.)
 //
 // Tile layouts: a CTA pair (cta_group::2) on a 256 x 256 tile by default; for
@@ -1355,7 +1357,11 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const bool pre = p.tma_epi && tma_rows && epi_inputs(p, ga) > 0 &&
                        n0 + half * (narrow ? BN / 4 : BN / 2) < ga.N;
       if (pre && lane == 0) epi_issue_inputs(p, gi, epi_inputs(p, ga), n0 + half * (narrow ? BN / 4 : BN / 2), trow, es);
-      const int ce_label = p.epi == tpi::EPI_CE && row0 + lane < ga.M ? p.ce_labels[row0 + lane] - g * ga.N : -1;
+      int ce_label = -1;  // this thread's row's, in the problem's columns; loaded while the MMAs run
+      if (p.epi == tpi::EPI_CE && row0 + lane < ga.M) {
+        const int l = p.ce_labels[row0 + lane];
+        ce_label = l < 0 ? -1 : l - g * ga.N;
+      }
       QGroup z0{}, z1{};
       const bool from_q = p.epi == tpi::EPI_DGELU_Q || p.epi == tpi::EPI_DSWIGLU_Q;
       if (from_q && p.tma_epi) {  // and so do its 8-bit groups

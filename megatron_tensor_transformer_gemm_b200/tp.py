@@ -275,7 +275,9 @@ def _use_shards(dev: int, name: str, ts, p: int, shape: tuple, *dtypes):
 
 def _on_device(dev: int, func: str, stream, *args) -> None:
     """Call lib.<func>(*args, stream) with device `dev` current: kernels launch on the current device."""
-    if dev < 0 or dev == torch.cuda.current_device():
+    if dev < 0:
+        raise ValueError(f"{func}: the tensors are on the CPU")
+    if dev == torch.cuda.current_device():
         check(getattr(lib, func)(*args, _stream(stream)), func)
     else:
         with torch.cuda.device(dev):

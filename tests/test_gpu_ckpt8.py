@@ -83,7 +83,7 @@ def _act_error(z, act):
 
 
 SHAPES = [  # T, h, f, p
-    (1, 64, 16, 1), (3, 128, 96, 2), (17, 512, 272, 1), (130, 256, 2048, 4), (300, 512, 1376, 2), (257, 72, 4096, 8), (641, 1024, 528, 1),
+    (5, 8, 16, 1), (1, 64, 16, 1), (3, 128, 96, 2), (17, 512, 272, 1), (130, 256, 2048, 4), (300, 512, 1376, 2), (257, 72, 4096, 8), (641, 1024, 528, 1),
 ]
 
 

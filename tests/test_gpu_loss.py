@@ -101,7 +101,7 @@ def _check(X, W, labels, V, scale, out, dtype):
 
 
 SHAPES = [  # T, h, V, p, chunk
-    (1, 64, 50, 1, 0), (2, 128, 1003, 2, 0), (17, 512, 1003, 2, 0), (129, 72, 3001, 1, 0),
+    (5, 8, 3, 1, 0), (130, 16, 9, 2, 7), (1, 64, 50, 1, 0), (2, 128, 1003, 2, 0), (17, 512, 1003, 2, 0), (129, 72, 3001, 1, 0),
     (300, 256, 777, 4, 0), (640, 512, 4096, 8, 0), (257, 1024, 20011, 4, 0), (513, 128, 260, 2, 0),
     (2500, 64, 131, 1, 0), (300, 256, 777, 4, 100), (1030, 128, 5003, 2, 256), (515, 136, 2048, 1, 513),
 ]

@@ -118,6 +118,8 @@ def test_gated_norm_binding_checks():
         call("layer", 8, x, x, x, stats=torch.zeros(2, 8))
     with pytest.raises(KeyError):
         call("batch", 8, x, x, x)
+    with pytest.raises(ValueError, match="on the CPU"):  # host memory never reaches a kernel
+        call("layer", 8, x, x, x)
 
 
 def _cfwd(plan, T=4, X=A, W=A, bias=None, Zq=A, Zs=A + 1, H=A):
@@ -190,6 +192,8 @@ def test_tensors_of_one_call_are_on_one_device(monkeypatch):
     tp._on_device(1, "f", 5, "a")
     tp._on_device(0, "f", 5, "b")
     assert seen == [(1, ("a", 5)), (0, ("b", 5))]
+    with pytest.raises(ValueError, match="f: the tensors are on the CPU"):
+        tp._on_device(-1, "f", 5, "c")
     with pytest.raises(ValueError, match="x: .* on cuda:1, got .* on cpu"):
         tp._use(1, "x", torch.zeros(3), (3,), torch.float32)
     with pytest.raises(ValueError, match=r"W\[0\]: .* on cuda:0, got .* on cpu"):
