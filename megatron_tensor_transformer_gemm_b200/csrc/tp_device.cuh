@@ -490,6 +490,18 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
+// Two values in [0, 2) in 16 bits each, the upper bits of their fp32 forms below
+// the exponent's first bit (which is zero): 7 bits of exponent and 9 of
+// significand, rounded to nearest, so off by at most 2^-10 of the value, over the
+// whole range of fp32 below 2 (fp16 has one bit more but ends at 2^-25, bf16 two
+// less).
+__device__ __forceinline__ uint32_t pack_unit16x2(float lo, float hi) {
+  return ((__float_as_uint(lo) + 0x2000u) >> 14) | (((__float_as_uint(hi) + 0x2000u) << 2) & 0xffff0000u);
+}
+__device__ __forceinline__ float2 unpack_unit16x2(uint32_t u) {
+  return make_float2(__uint_as_float((u & 0xffffu) << 14), __uint_as_float((u >> 16) << 14));
+}
+
 // 8-bit groups: 32 values as e4m3 codes times one power of two, the least (at
 // least 2^-126) that brings their largest magnitude to at most 448, the format's
 // largest: no value saturates, and a power of two adds no rounding of its own,

@@ -636,10 +636,10 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
 // Cross-entropy epilogue (EPI_CE): a thread has one row and takes its columns 64
 // at a time (a slot), which it holds in registers: their largest score, the
 // exponentials relative to it, their sum, and, when gradients follow, the
-// exponentials themselves in bf16: one rounding (2^-8) beside the gradient's own,
-// with fp32's range, so that an entry far below its slot's largest keeps its
-// gradient (fp16 would be 2^-11 but lose what is below 2^-25). The scores exist
-// only here, in fp32. Padding columns and the row's label (`label`, as a column of
+// exponentials themselves in 16 bits (pack_unit16x2: 2^-10, against the 2^-8 of the
+// gradient's own rounding to bf16; bf16 here too made the gradients' error 1.9
+// times that of a single rounding, and fp16 lost entries below 2^-25 of their
+// slot's largest). The scores exist only here, in fp32. Padding columns and the row's label (`label`, as a column of
 // this problem) take no part: the label's score is added in full precision later.
 // Slots of 128 columns in two passes over TMEM, whose load latency they paid eight
 // times a tile, took about 8000 clocks a tile; K = 512 has 4096 of MMAs.
@@ -667,7 +667,7 @@ __device__ __forceinline__ float ce_exps(const float (&v)[32], float mo, uint32_
   for (int i = 0; i < 32; i += 2) {
     const float a = ex2(fmaf(v[i], kLog2e, -mo)), b = ex2(fmaf(v[i + 1], kLog2e, -mo));
     s[(i / 2) & 3] += a + b;
-    h[i / 2] = pack_bf16x2(a, b);
+    h[i / 2] = pack_unit16x2(a, b);
   }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }

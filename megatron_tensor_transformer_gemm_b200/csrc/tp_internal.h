@@ -290,7 +290,7 @@ struct GemmBatch {
   // largest score times log2 e and s the sum of 2^(score log2 e - m) over the
   // slot's columns except padding and the row's label (both count as exp 0; m =
   // -inf if none is left). A slot without columns may not be written. D (optional)
-  // holds those exps in bf16.
+  // holds those exps in 16 bits (tp_device.cuh pack_unit16x2).
   int ce_vocab;
   const int32_t* ce_labels;
   float2* ce_stats;

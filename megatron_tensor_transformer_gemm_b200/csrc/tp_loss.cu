@@ -8,8 +8,8 @@
 // Tokens are taken a chunk at a time. For bf16 plans the scores live only in the
 // tensor cores' fp32 accumulators: the GEMM's epilogue leaves, per row and slot of
 // 64 columns, their maximum m and sum of 2^(z log2 e - m), and, when
-// gradients are wanted, the exponentials themselves in bf16 (relative to the slot's
-// maximum). A row kernel merges the slots (the running maximum and sum of a
+// gradients are wanted, the exponentials themselves in 16 bits (relative to the
+// slot's maximum). A row kernel merges the slots (the running maximum and sum of a
 // softmax, joined), adds the label's score, and turns the exponentials into d in
 // place with one factor 2^(m - lse2) * scale per slot; then the two products. So
 // each score is computed once: 6 T V h operations for loss and gradients, against
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
     float d[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float2 v = tpd::unpack_bf16x2(w[q]);
+      const float2 v = tpd::unpack_unit16x2(w[q]);
       d[2 * q] = v.x * f;
       d[2 * q + 1] = v.y * f;
     }
