@@ -314,6 +314,7 @@ __device__ __forceinline__ void dswiglu_q(const QGroup& g8, const QGroup& u8, fl
 }
 
 // Columns [half * BN/2, (half + 1) * BN/2) of the accumulator row this thread owns.
+template <bool Q8>
 __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t taddr, int row,
                               int n0, int half, bool narrow, int ks) {
   const bool row_ok = row < ga.M;
@@ -332,7 +333,7 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
           store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, g);
           store_row_chunk_bf16(static_cast<__nv_bfloat16*>(ga.D) + ga.nh, ga.ldd, row, j0, ga.N, u);
         }
-        if (ga.q) {
+        if (Q8 && ga.q) {
           q_store(ga, row, j0, 0, g);
           q_store(ga, row, j0, 1, u);
         }
@@ -398,7 +399,7 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
           for (int i = 0; i < 32; ++i) v[i] += b[i];
         }
         if (ga.D) store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, v);
-        if (ga.q) q_store(ga, row, j0, 0, v);
+        if (Q8 && ga.q) q_store(ga, row, j0, 0, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i]);
         store_row_chunk_bf16(ga.D2, ga.ldd2, row, j0, ga.N, v);
@@ -429,6 +430,7 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
         break;
       }
       case tpi::EPI_DGELU_Q: {
+        if constexpr (!Q8) break;
         float h[32];
         dgelu_q(q_load(ga, row, j0, 0), v, h);
         store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, v);
@@ -436,6 +438,7 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
         break;
       }
       case tpi::EPI_DSWIGLU_Q: {
+        if constexpr (!Q8) break;
         float dg[32], h[32];
         dswiglu_q(q_load(ga, row, j0, 0), q_load(ga, row, j0, 1), dg, v, h);
         store_row_chunk_bf16(ga.D, ga.ldd, row, j0, ga.N, dg);
@@ -554,6 +557,7 @@ __device__ __forceinline__ void epi_issue_inputs(const GemmParams& p, int gi, in
 // Forward activation epilogues through the stage (nothing staged in): SwiGLU
 // stores Z = [g | u] (when requested, through tmE) and H = SiLU(g) u (tmX);
 // bias + GELU stores Z (when requested, tmE) and H = GELU(Z) (tmX).
+template <bool Q8>
 __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int gi, uint32_t taddr, int row0,
                                  int n0, int half, bool narrow, int lane, EpiStage& es) {
   uint8_t* t = es.buf;
@@ -569,7 +573,7 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
       tmem_ld32(taddr + c * 32, g);
       tmem_ld32(taddr + 128 + c * 32, u);
       tc_wait_ld();
-      if (ga.q && row0 + lane < ga.M) {
+      if (Q8 && ga.q && row0 + lane < ga.M) {
         q_store(ga, row0 + lane, j0, 0, g);
         q_store(ga, row0 + lane, j0, 1, u);
       }
@@ -619,7 +623,7 @@ __device__ void epilogue_fwd_tma(const GemmParams& p, const GroupArgs& ga, int g
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
     if (ga.D) stage_write(t0, lane, v);
-    if (ga.q && row0 + lane < ga.M) q_store(ga, row0 + lane, j0, 0, v);
+    if (Q8 && ga.q && row0 + lane < ga.M) q_store(ga, row0 + lane, j0, 0, v);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i]);
     stage_write(t1, lane, v);
@@ -1053,7 +1057,12 @@ __device__ __forceinline__ Tile ring_take_warp(const TileRing& r, int k, uint32_
 }
 
 // -------------------------------------------------------------------- kernel
-template <int PAIR>
+// Instances by what their epilogues do: kPlain, kHead (EPI_CE) and kEight (8-bit
+// pre-activations, written or read). In one kernel the epilogues share its
+// registers: with all of them in it, the 12-layer stack's short launches took 3 %
+// longer (4.03 against 3.89 ms a step).
+enum { kPlain = 0, kHead = 1, kEight = 2 };
+template <int PAIR, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_constant__ GemmParams p) {
   using C = Cfg<PAIR>;
   constexpr int STAGES = C::STAGES;
@@ -1333,7 +1342,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
     uint32_t acc_phase = 0;
     const uint32_t tempty_leader = PAIR == 2 ? map_shared(smem_u32(&tempty[0]), 0) : 0u;
     EpiStage es{sE + (warp - 2) * kEpiBuf, &ebar[warp - 2], 0u, 0};
-    CeStats ce_out{};
+    [[maybe_unused]] CeStats ce_out{};
     bool ok = true;
     for (int kseq = 0;; ++kseq) {
       const Tile tile = ring_take_warp<PAIR>(ring, kseq, rank, lane, abort_flag, p.status);
@@ -1357,17 +1366,24 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const bool pre = p.tma_epi && tma_rows && epi_inputs(p, ga) > 0 &&
                        n0 + half * (narrow ? BN / 4 : BN / 2) < ga.N;
       if (pre && lane == 0) epi_issue_inputs(p, gi, epi_inputs(p, ga), n0 + half * (narrow ? BN / 4 : BN / 2), trow, es);
-      int ce_label = -1;  // this thread's row's, in the problem's columns; loaded while the MMAs run
-      if (p.epi == tpi::EPI_CE && row0 + lane < ga.M) {
-        const int l = p.ce_labels[row0 + lane];
-        ce_label = l < 0 ? -1 : l - g * ga.N;
+      // inputs loaded while the MMAs run: this thread's row's label, as a column of
+      // the problem, or its first 8-bit groups
+      [[maybe_unused]] int ce_label = -1;
+      [[maybe_unused]] QGroup z0, z1;
+      [[maybe_unused]] const bool from_q = p.epi == tpi::EPI_DGELU_Q || p.epi == tpi::EPI_DSWIGLU_Q;
+      if constexpr (KIND == kHead) {
+        if (row0 + lane < ga.M) {
+          const int l = p.ce_labels[row0 + lane];
+          ce_label = l < 0 ? -1 : l - g * ga.N;
+        }
       }
-      QGroup z0{}, z1{};
-      const bool from_q = p.epi == tpi::EPI_DGELU_Q || p.epi == tpi::EPI_DSWIGLU_Q;
-      if (from_q && p.tma_epi) {  // and so do its 8-bit groups
-        const int j0 = n0 + half * (narrow ? BN / 4 : BN / 2);
-        z0 = q_load(ga, row0 + lane, j0, 0);
-        if (p.epi == tpi::EPI_DSWIGLU_Q) z1 = q_load(ga, row0 + lane, j0, 1);
+      if constexpr (KIND == kEight) {
+        z0 = z1 = QGroup{};
+        if (from_q && p.tma_epi) {
+          const int j0 = n0 + half * (narrow ? BN / 4 : BN / 2);
+          z0 = q_load(ga, row0 + lane, j0, 0);
+          if (p.epi == tpi::EPI_DSWIGLU_Q) z1 = q_load(ga, row0 + lane, j0, 1);
+        }
       }
       // warp-uniform: the epilogue's tcgen05.ld is warp-collective
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.status))) {
@@ -1378,17 +1394,19 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      ce_out.store();
+      if constexpr (KIND == kHead) ce_out.store();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(lg * 32) << 16) +
                              static_cast<uint32_t>(acc * BN);
-      if (p.tma_epi && !tma_rows) {
-        // past the last row of a scattered launch: nothing to store
-      } else if (p.epi == tpi::EPI_CE) {
+      if constexpr (KIND == kHead) {
         epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, ce_label, es, ce_out);
+      } else if constexpr (KIND == kEight) {
+        if (!p.tma_epi) epilogue_tile<true>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
+        else if (from_q) epilogue_bwd_q_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es, z0, z1);
+        else epilogue_fwd_tma<true>(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
+      } else if (p.tma_epi && !tma_rows) {
+        // past the last row of a scattered launch: nothing to store
       } else if (p.tma_epi && (p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU)) {
-        epilogue_fwd_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
-      } else if (p.tma_epi && from_q) {
-        epilogue_bwd_q_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es, z0, z1);
+        epilogue_fwd_tma<false>(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi && p.epi == tpi::EPI_STORE && epi_inputs(p, ga) == 0) {
         epilogue_store_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi) {
@@ -1396,7 +1414,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       } else if (p.plain_staged) {
         epilogue_plain_staged(p, ga, taddr, row0, n0, half, narrow, lane, smem_u32(es.buf));
       } else {
-        epilogue_tile(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
+        epilogue_tile<false>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
       }
       if (!ok) break;
       tc_fence_before();
@@ -1408,7 +1426,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-    ce_out.store();
+    if constexpr (KIND == kHead) ce_out.store();
     if (p.tma_epi && lane == 0) bulk_wait_all();  // every store of this warp has landed
   }
 
@@ -1595,23 +1613,23 @@ Layout choose_layout(const GemmBatch& b, int sms, double* cost_out = nullptr) {
   return best;
 }
 
-template <int PAIR>
+template <int PAIR, int KIND>
 tp_status launch_kernel(const GemmParams& p, int tiles, int sms, cudaStream_t st) {
   using C = Cfg<PAIR>;
   constexpr int kMaxDev = 64;
-  static bool attr_set[kMaxDev][2] = {};
+  static bool attr_set[kMaxDev] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) {
     cudaGetLastError();
     return tpi::fail(TP_ERR_NO_DEVICE, "no current CUDA device");
   }
-  if (!attr_set[dev][PAIR - 1]) {
+  if (!attr_set[dev]) {
     tp_status s = tpi::cuda_status(
-        cudaFuncSetAttribute(tp_gemm_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(tp_gemm_kernel<PAIR, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM_BYTES),
         "cudaFuncSetAttribute(gemm smem)");
     if (s != TP_OK) return s;
-    attr_set[dev][PAIR - 1] = true;
+    attr_set[dev] = true;
   }
   const int clusters = std::max(1, std::min(tiles, sms / PAIR));
   cudaLaunchConfig_t cfg{};
@@ -1628,7 +1646,7 @@ tp_status launch_kernel(const GemmParams& p, int tiles, int sms, cudaStream_t st
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = tpi::pdl_enabled() ? 2 : 1;
-  tp_status s = tpi::cuda_status(cudaLaunchKernelEx(&cfg, tp_gemm_kernel<PAIR>, p),
+  tp_status s = tpi::cuda_status(cudaLaunchKernelEx(&cfg, tp_gemm_kernel<PAIR, KIND>, p),
                                  "cudaLaunchKernelEx(gemm)");
   if (s != TP_OK) return s;
   return tpi::after_launch(PAIR == 2 ? "gemm_bf16 (tcgen05, CTA pair)" : "gemm_bf16 (tcgen05)");
@@ -1894,8 +1912,9 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
     s = sched_slot(st, &p.sched);
     if (s != TP_OK) return s;
   }
-  if (pair == 2) return launch_kernel<2>(p, tiles, sms, st);
-  return launch_kernel<1>(p, tiles, sms, st);
+  if (b.epi == EPI_CE) return pair == 2 ? launch_kernel<2, kHead>(p, tiles, sms, st) : launch_kernel<1, kHead>(p, tiles, sms, st);
+  if (b.g[0].q) return pair == 2 ? launch_kernel<2, kEight>(p, tiles, sms, st) : launch_kernel<1, kEight>(p, tiles, sms, st);
+  return pair == 2 ? launch_kernel<2, kPlain>(p, tiles, sms, st) : launch_kernel<1, kPlain>(p, tiles, sms, st);
 }
 
 bool gemm_fills_gpu(const GemmBatch& b) {
