@@ -319,9 +319,10 @@ TP_API tp_status tp_vocab_cross_entropy(tp_plan* plan, int64_t T, const void* co
  *   int32 (device; < 0 = ignored token, >= vocab sets the device status and is
  *   ignored). loss [T] fp32 = logsumexp over the real vocab columns minus the
  *   target score (0 for ignored tokens); lse [T] fp32 (NULL ok).
- *   dX [T, hidden] (NULL skips) = sum_i d_i W[i] and dW[i] [Vp/p, hidden] (NULL
- *   array skips) = d_i^T X, with d = (softmax - onehot) * grad_scale, rounded to
- *   the plan dtype before the two products; sums are fp32 and rounded once.
+ *   dX [T, hidden] (NULL skips) = grad_scale * sum_i d_i W[i] and dW[i] [Vp/p,
+ *   hidden] (NULL array skips) = grad_scale * d_i^T X, with d = softmax - onehot
+ *   rounded to the plan dtype before the two products; sums are fp32 and rounded
+ *   once, scaled.
  *   Padding rows of dW are zero. dX and dW must not alias X and W.
  *   chunk: tokens whose scores are worked on at a time (0: the library's choice);
  *   the workspace holds them as 2 (bf16) or 4 (fp32) bytes per token and padded
@@ -441,7 +442,7 @@ TP_API tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void
 /* tp_row_bwd of the MLP from the pre-activation kept by tp_column_fwd_ckpt8:
  * with Z decoded from Zq and Zs in the GEMM's epilogue, dZ[i] as in tp_row_bwd,
  * H[i] [T, ffn/p] = the activation of the decoded Z (NULL array skips when dW is
- * NULL), dW[i] = dY^T H[i] with that H, and dbias. Everything runs on `stream`
+ * NULL; not dZ[i]), dW[i] = dY^T H[i] with that H, and dbias. Everything runs on `stream`
  * (the deferred and grouped modes do not apply; a waiting weight gradient is
  * launched first). Uses the plan's workspace: make a call of the same sizes before
  * capturing one. With T = 0, dW and dbias are set to zero. */

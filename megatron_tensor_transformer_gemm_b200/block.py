@@ -55,6 +55,8 @@ class TPMLP:
         between the passes the MLP holds 1.03 bytes per pre-activation element in
         place of the 2 of Z and the 2 of H. H is then scratch within a pass:
         H_scratch (a list of p [T, ffn/p] tensors) lets layers share it."""
+        if H_scratch is not None and not ckpt8:
+            raise ValueError("H_scratch needs ckpt8: without it H is kept from the forward for the backward")
         self.ckpt8, self._H_scratch = ckpt8, H_scratch
         self.h, self.f, self.p, self.act = hidden, ffn, p, act
         self.fused = fused

@@ -1314,9 +1314,13 @@ tp_status tp_vocab_linear_cross_entropy(tp_plan* plan, int64_t T, const void* X,
   TP_TRY(check_row_bytes(h, plan->dtype, "hidden"));
   // gradients overwrite nothing that a later step of the call reads
   if (T > 0 && dX == X) return fail(TP_ERR_ARG, "dX must not alias X");
-  for (int i = 0; dW && i < p; ++i)
+  for (int i = 0; i < p; ++i) {
+    if (T > 0 && dX && dX == W[i]) return fail(TP_ERR_ARG, "dX must not alias W[%d]", i);
+    if (!dW) continue;
+    if (T > 0 && (dW[i] == X || dW[i] == dX)) return fail(TP_ERR_ARG, "dW[%d] must not alias X or dX", i);
     for (int j = 0; j < p; ++j)
       if (dW[i] == W[j]) return fail(TP_ERR_ARG, "dW[%d] must not alias W[%d]", i, j);
+  }
   cudaStream_t st = as_stream(stream);
   if (dW) TP_TRY(flush_wgrad(plan));
   if (T == 0) {  // no token: the weight gradient is zero
@@ -1852,6 +1856,8 @@ tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void*
   TP_TRY(check_scales(Zs, p));
   TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(H), p, "H", true));
   TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dZ), p, "dZ", false));
+  for (int i = 0; H && i < p; ++i)
+    if (H[i] == dZ[i]) return fail(TP_ERR_ARG, "H[%d] must not alias dZ[%d]", i, i);
   note_capture(plan, st);
   GemmBatch b{};
   b.n = p;

@@ -361,8 +361,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
   // thread 0's: the next row to load and its stage, rows whose loads are not issued
   __shared__ Walk ahead;
   __shared__ int in_stage, to_issue;
-  auto issue = [&]() {  // thread 0
+  auto issue = [&]() {  // thread 0, after a barrier behind the stage's last use
     Walk w = ahead;
+    tpd::fence_proxy_async_smem();  // the threads' own writes to the stage come before the copies'
     const int64_t off = w.t * p.h + static_cast<int64_t>(v0) * N;
     uint8_t* dst = sbuf + static_cast<uint32_t>(in_stage) * stage_bytes;
     uint64_t* br = &bar[in_stage];

@@ -79,6 +79,13 @@ struct Cfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory of the GEMM kernel");
 };
 
+// Instances of the kernel by what their epilogues do: kPlain, kHead (the output
+// head with its loss: EPI_CE, and EPI_STORE times alpha for its gradients) and
+// kEight (8-bit pre-activations, written or read). In one kernel the epilogues
+// share its registers: with all of them in it, the 12-layer stack's short launches
+// took 3 % longer (4.03 against 3.89 ms a step).
+enum { kPlain = 0, kHead = 1, kEight = 2 };
+
 struct GroupArgs {
   int M, N, K;
   int tiles_n;
@@ -157,6 +164,7 @@ struct alignas(64) GemmParams {
   const int32_t* ce_labels;
   float2* ce_stats;
   int64_t ce_pairs;
+  float alpha;  // kHead's EPI_STORE
   CUtensorMap tmE[TP_MAX_SHARDS];
   CUtensorMap tmX[TP_MAX_SHARDS];
   unsigned* status;
@@ -317,11 +325,12 @@ __device__ __forceinline__ void dswiglu_q(const QGroup& g8, const QGroup& u8, fl
 }
 
 // Columns [half * BN/2, (half + 1) * BN/2) of the accumulator row this thread owns.
-template <bool Q8>
+template <int KIND>
 __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t taddr, int row,
                               int n0, int half, bool narrow, int ks) {
+  constexpr bool Q8 = KIND == kEight;
   const bool row_ok = row < ga.M;
-  if (p.epi == tpi::EPI_SWIGLU) {
+  if (KIND != kHead && p.epi == tpi::EPI_SWIGLU) {
     // Accumulator columns [0,128) = gate units n0.., [128,256) = the same up units;
     // this thread handles gate/up pairs [half * 64, half * 64 + 64).
 #pragma unroll 1
@@ -356,9 +365,13 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
     tc_wait_ld();
     const int j0 = n0 + c * 32;
     if (!row_ok || j0 >= ga.N) continue;
-    switch (p.epi) {
+    switch (KIND == kHead ? static_cast<int>(tpi::EPI_STORE) : p.epi) {
       case tpi::EPI_STORE: {
-        if (ga.bias) {
+        if constexpr (KIND == kHead) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= p.alpha;
+        }
+        if (KIND != kHead && ga.bias) {
           float b[32];
           load_row_chunk_bf16(ga.bias, 0, 0, j0, ga.N, b);
 #pragma unroll
@@ -368,13 +381,13 @@ __device__ void epilogue_tile(const GemmParams& p, const GroupArgs& ga, uint32_t
         if (ks) dst = static_cast<float*>(dst) + ks * p.split_stride;  // split K: fp32 partials
         const void* res = ga.aux;
         int orow = row;
-        if (p.scatter) {
+        if (KIND != kHead && p.scatter) {
           const int j = row / p.rows_per_out;
           orow = row - j * p.rows_per_out;
           dst = p.out_seq[j];
           res = p.res_seq[j];
         }
-        if (res) {
+        if (KIND != kHead && res) {
           float r[32];
           load_row_chunk_bf16(res, ga.ldaux, orow, j0, ga.N, r);
 #pragma unroll
@@ -774,6 +787,7 @@ __device__ void epilogue_ce(const GemmParams& p, const GroupArgs& ga, int g, uin
 
 // Plain bf16 outputs without staged inputs, 64 columns at a time: both tiles of
 // the stage fill after one wait for TMEM and leave after one fence.
+template <int KIND>
 __device__ void epilogue_store_tma(const GemmParams& p, const GroupArgs& ga, int gi, uint32_t taddr, int row0, int n0,
                                    int half, bool narrow, int lane, EpiStage& es) {
   const int pairs = narrow ? 1 : 2;
@@ -787,7 +801,13 @@ __device__ void epilogue_store_tma(const GemmParams& p, const GroupArgs& ga, int
     tmem_ld32(taddr + c * 64, v);
     tmem_ld32(taddr + c * 64 + 32, w);
     tc_wait_ld();
-    if (ga.bias) {
+    if constexpr (KIND == kHead) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] *= p.alpha;
+        w[i] *= p.alpha;
+      }
+    } else if (ga.bias) {
       float b[32];
       load_row_chunk_bf16(ga.bias, 0, 0, j0, ga.N, b);
 #pragma unroll
@@ -1064,11 +1084,6 @@ __device__ __forceinline__ Tile ring_take_warp(const TileRing& r, int k, uint32_
 }
 
 // -------------------------------------------------------------------- kernel
-// Instances by what their epilogues do: kPlain, kHead (EPI_CE) and kEight (8-bit
-// pre-activations, written or read). In one kernel the epilogues share its
-// registers: with all of them in it, the 12-layer stack's short launches took 3 %
-// longer (4.03 against 3.89 ms a step).
-enum { kPlain = 0, kHead = 1, kEight = 2 };
 template <int PAIR, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_constant__ GemmParams p) {
   using C = Cfg<PAIR>;
@@ -1379,7 +1394,7 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       [[maybe_unused]] QGroup z0, z1;
       [[maybe_unused]] const bool from_q = p.epi == tpi::EPI_DGELU_Q || p.epi == tpi::EPI_DSWIGLU_Q;
       if constexpr (KIND == kHead) {
-        if (row0 + lane < ga.M) {
+        if (p.epi == tpi::EPI_CE && row0 + lane < ga.M) {
           const int l = p.ce_labels[row0 + lane];
           ce_label = l < 0 ? -1 : l - g * ga.N;
         }
@@ -1405,9 +1420,11 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(lg * 32) << 16) +
                              static_cast<uint32_t>(acc * BN);
       if constexpr (KIND == kHead) {
-        epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, ce_label, es, ce_out);
+        if (p.epi == tpi::EPI_CE) epilogue_ce(p, ga, g, taddr, row0, n0, half, narrow, lane, ce_label, es, ce_out);
+        else if (p.tma_epi) epilogue_store_tma<KIND>(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
+        else epilogue_tile<KIND>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
       } else if constexpr (KIND == kEight) {
-        if (!p.tma_epi) epilogue_tile<true>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
+        if (!p.tma_epi) epilogue_tile<KIND>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
         else if (from_q) epilogue_bwd_q_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es, z0, z1);
         else epilogue_fwd_tma<true>(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi && !tma_rows) {
@@ -1415,13 +1432,13 @@ __global__ void __launch_bounds__(kThreads, 1) tp_gemm_kernel(const __grid_const
       } else if (p.tma_epi && (p.epi == tpi::EPI_SWIGLU || p.epi == tpi::EPI_BIAS_GELU)) {
         epilogue_fwd_tma<false>(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi && p.epi == tpi::EPI_STORE && epi_inputs(p, ga) == 0) {
-        epilogue_store_tma(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
+        epilogue_store_tma<KIND>(p, ga, gi, taddr, trow, n0, half, narrow, lane, es);
       } else if (p.tma_epi) {
         ok = epilogue_tile_tma(p, ga, gi, taddr, trow, n0, half, narrow, pre, lane, es, abort_flag, p.status);
       } else if (p.plain_staged) {
         epilogue_plain_staged(p, ga, taddr, row0, n0, half, narrow, lane, smem_u32(es.buf));
       } else {
-        epilogue_tile<false>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
+        epilogue_tile<KIND>(p, ga, taddr, row0 + lane, n0, half, narrow, ks);
       }
       if (!ok) break;
       tc_fence_before();
@@ -1902,6 +1919,12 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
   p.b_mn = b.b_mn;
   p.epi = b.epi;
   p.out_f32 = b.out_f32;
+  if (b.scaled) {
+    bool plain = b.epi == EPI_STORE && !b.scatter_n && !b.plain_stores;
+    for (int i = 0; i < nout; ++i) plain = plain && !b.g[i].bias && !b.g[i].aux;
+    if (!plain) return fail(TP_ERR_ARG, "a scaled GEMM has a plain epilogue");
+    p.alpha = b.alpha;
+  }
   if (b.epi == EPI_CE) {
     for (int i = 1; i < b.n; ++i)
       if (b.g[i].N != b.g[0].N) return fail(TP_ERR_ARG, "cross-entropy GEMM: problem %d has another width", i);
@@ -1919,7 +1942,7 @@ tp_status launch_gemm_bf16(const GemmBatch& b, cudaStream_t st) {
     s = sched_slot(st, &p.sched);
     if (s != TP_OK) return s;
   }
-  if (b.epi == EPI_CE) return pair == 2 ? launch_kernel<2, kHead>(p, tiles, sms, st) : launch_kernel<1, kHead>(p, tiles, sms, st);
+  if (b.epi == EPI_CE || b.scaled) return pair == 2 ? launch_kernel<2, kHead>(p, tiles, sms, st) : launch_kernel<1, kHead>(p, tiles, sms, st);
   if (b.g[0].q) return pair == 2 ? launch_kernel<2, kEight>(p, tiles, sms, st) : launch_kernel<1, kEight>(p, tiles, sms, st);
   return pair == 2 ? launch_kernel<2, kPlain>(p, tiles, sms, st) : launch_kernel<1, kPlain>(p, tiles, sms, st);
 }

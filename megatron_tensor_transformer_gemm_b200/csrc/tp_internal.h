@@ -283,6 +283,9 @@ struct GemmBatch {
   // Outputs that may be another GPU's memory (a peer group's receive
   // buffers): the epilogue writes them with plain stores, never TMA.
   bool plain_stores;
+  // EPI_STORE without bias, residual or scatter: D = alpha * product (+ acc).
+  bool scaled;
+  float alpha;
   // EPI_CE: problem i's columns are vocab entries [i * N, (i + 1) * N), those
   // from ce_vocab on padding. A slot is 64 columns of a problem, and a pair of
   // slots (S = ceil(N / 128) pairs) has four floats per row: ce_stats[2 * (r *

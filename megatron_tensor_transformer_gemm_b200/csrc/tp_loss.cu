@@ -3,7 +3,7 @@
 // head weight from X and W, without keeping the scores z = X W^T.
 //
 //   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label
-//   d_tv  = (exp(z_tv - lse_t) - [v = label]) * scale,  dX = d W,  dW = d^T X
+//   d_tv  = exp(z_tv - lse_t) - [v = label],  dX = scale * d W,  dW = scale * d^T X
 //
 // Tokens are taken a chunk at a time. For bf16 plans the scores live only in the
 // tensor cores' fp32 accumulators: the GEMM's epilogue leaves, per row and slot of
@@ -11,7 +11,9 @@
 // gradients are wanted, the exponentials themselves in 16 bits (relative to the
 // slot's maximum). A row kernel merges the slots (the running maximum and sum of a
 // softmax, joined), adds the label's score, and turns the exponentials into d in
-// place with one factor 2^(m - lse2) * scale per slot; then the two products. So
+// place with one factor 2^(m - lse2) per slot; then the two products, whose
+// epilogues apply the scale (in d's rounding to bf16 the labels' entries, all near
+// -scale, would share one error, up to 2^-9 of the gradients). So
 // each score is computed once: 6 T V h operations for loss and gradients, against
 // 8 for recomputing the scores in the backward, at 6 bytes of traffic per score.
 // fp32 plans keep the chunk's scores in fp32.
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
 constexpr int kFinThreads = 256;
 __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
     const float4* stats, int shard_pairs, const __nv_bfloat16* X,
-    const __grid_constant__ PtrArray W, int h, int vocab, int Vs, int p, const int32_t* labels, float scale, float* loss,
+    const __grid_constant__ PtrArray W, int h, int vocab, int Vs, int p, const int32_t* labels, float* loss,
     float* lse_out, uint4* e, unsigned* status) {
   tpd::pdl_entry();
   __shared__ float2 red[kFinThreads / 32];
@@ -167,14 +169,14 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
     for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) row[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const float at_label = (tpd::ex2(z2 - lse2) - 1.f) * scale;
+  const float at_label = tpd::ex2(z2 - lse2) - 1.f;
 #pragma unroll 4
   for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) {
     const uint4 u = row[i];
     const int sh = i / nv, c = (i - sh * nv) * 8;
     const float4* at = st + sh * shard_pairs + c / 128;
     const float m = c & 64 ? at->z : at->x;  // -inf: all its exps are 0
-    const float f = tpd::ex2(m - lse2) * scale;
+    const float f = tpd::ex2(m - lse2);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     float d[8];
 #pragma unroll
@@ -295,6 +297,8 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.b_mn = true;
     b.epi = EPI_STORE;
     b.kcat = true;
+    b.scaled = true;
+    b.alpha = scale;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
       g.M = static_cast<int>(n);
@@ -314,6 +318,8 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.n = p;
     b.a_mn = b.b_mn = true;
     b.epi = EPI_STORE;
+    b.scaled = true;
+    b.alpha = scale;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
       g.M = Vs;
@@ -376,7 +382,7 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     const int64_t parts = grad ? std::max<int64_t>(1, std::min<int64_t>(512 / n, Vp / 8 / kFinThreads)) : 1;
     (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
                  reinterpret_cast<const float4*>(stats), shard_pairs, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
-                 V, Vs, p, labels + t0, scale, loss + t0, lse ? lse + t0 : nullptr,
+                 V, Vs, p, labels + t0, loss + t0, lse ? lse + t0 : nullptr,
                  grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
     TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
     if (dX) {

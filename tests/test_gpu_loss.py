@@ -241,3 +241,23 @@ def test_gradient_by_differences():
     diff = (total(e) - total(-e)) / (2 * e)
     got = float((torch.from_numpy(host(dX)) * U).sum() + (torch.from_numpy(np.concatenate([host(w) for w in dW])) * S).sum())
     assert abs(got - diff) <= 1e-4 * abs(diff) + 1e-4
+
+
+@pytest.mark.parametrize("T,chunk", [(40, 0), (515, 0), (515, 200)])
+def test_the_scale_is_not_rounded_with_d(T, chunk):
+    """A scale halfway between two bf16 values. Rounded with d, every label's entry (near
+    -scale where the softmax is small) would be off by nearly the same 2^-8 / (1 + 2^-8) =
+    0.0039, and so would dX. With d rounded before the scale, that entry, softmax - 1, is off
+    by at most its softmax, 2^-11 in the mean here. What stays is the result's rounding,
+    uniform within half a step of at most 2^-8 of the value, so at most 2^-8 / sqrt(3) =
+    0.00226 in the mean square, and the other entries' roundings: 2^-8 of terms whose sum
+    is below a hundredth of the label's row."""
+    V, scale = 4000, (1 + 2.0 ** -8) / 512
+    plan, Vp, X, W, labels = _head(T, 256, V, 2, "bf16", seed=T, ignored=False)
+    out = _run(plan, Vp, X, W, labels, scale, chunk)
+    _check(X, W, labels, V, scale, out, "bf16")
+    z = X.double() @ W[:V].double().T
+    assert float(torch.softmax(z, 1).gather(1, labels.long()[:, None]).mean()) < 2.0 ** -11
+    rx = _reference(X, W, labels, V, scale)[2]
+    err = float((torch.from_numpy(host(out[2])) - rx).norm() / rx.norm())
+    assert err < 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -11 + 2.0 ** -8 / 100

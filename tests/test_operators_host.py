@@ -198,3 +198,20 @@ def test_tensors_of_one_call_are_on_one_device(monkeypatch):
         tp._use(1, "x", torch.zeros(3), (3,), torch.float32)
     with pytest.raises(ValueError, match=r"W\[0\]: .* on cuda:0, got .* on cpu"):
         tp._use_shards(0, "W", [torch.zeros(3)], 1, (3,), torch.float32)
+
+
+def test_outputs_that_alias_what_a_call_reads(head):
+    assert _loss(head, dX=A + 32) == 1 and "W[1]" in tp.last_error()
+    assert _loss(head, dW=(A + 48, A)) == 1 and "dW[1]" in tp.last_error()
+    assert _loss(head, dX=A + 48, dW=(A + 48, A + 64)) == 1 and "dW[0]" in tp.last_error()
+    plan = tp.Plan(64, 64, 0, 2, "bf16", "gelu")
+    call = lambda H: tp.lib.tp_row_bwd_ckpt8(plan.handle, 4, A, _arr(A, A), _arr(A, A), _arr(A, A), H,  # noqa: E731
+                                             _arr(A + 16, A + 32), None, None, None)
+    assert call(_arr(A + 48, A + 32)) == 1 and "H[1]" in tp.last_error()
+
+
+def test_a_kept_activation_is_not_shared():
+    from megatron_tensor_transformer_gemm_b200.block import TPMLP
+    H = [torch.zeros(4, 32).bfloat16() for _ in range(2)]
+    with pytest.raises(ValueError, match="ckpt8"):
+        TPMLP(64, 64, 2, device="cpu", H_scratch=H)
