@@ -442,10 +442,11 @@ TP_API tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void
 /* tp_row_bwd of the MLP from the pre-activation kept by tp_column_fwd_ckpt8:
  * with Z decoded from Zq and Zs in the GEMM's epilogue, dZ[i] as in tp_row_bwd,
  * H[i] [T, ffn/p] = the activation of the decoded Z (NULL array skips when dW is
- * NULL; not dZ[i]), dW[i] = dY^T H[i] with that H, and dbias. Everything runs on `stream`
- * (the deferred and grouped modes do not apply; a waiting weight gradient is
- * launched first). Uses the plan's workspace: make a call of the same sizes before
- * capturing one. With T = 0, dW and dbias are set to zero. */
+ * NULL; not dZ[i]), dW[i] = dY^T H[i] with that H, and dbias. The products run on
+ * `stream` (the deferred and grouped modes do not apply; a waiting weight gradient
+ * is launched first), dbias beside them on the device's side stream, which `stream`
+ * waits for before the call returns. Uses the plan's workspace: make a call of the
+ * same sizes before capturing one. With T = 0, dW and dbias are set to zero. */
 TP_API tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void* const* W,
                                   const void* const* Zq, const uint8_t* const* Zs, void* const* H,
                                   void* const* dZ, void* const* dW, float* dbias, void* stream);

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_helpers import dev
+from gpu_helpers import dev, host
 
 pytestmark = pytest.mark.gpu
 EPS = 2.0 ** -24
@@ -268,3 +268,47 @@ def test_no_token():
     dW, db = [torch.ones_like(w)], torch.ones(64, device="cuda")
     plan.row_bwd_ckpt8(0, none, [w], q, s, [none], [none], dW, db)
     assert float(dW[0].abs().max()) == 0 and float(db.abs().max()) == 0
+
+
+@pytest.mark.parametrize("defer", [False, True])
+@pytest.mark.parametrize("concurrent", ["1", "0"])
+def test_backward_on_a_stream_and_replayed(defer, concurrent, monkeypatch):
+    """Every output is ready on the caller's stream when the call returns, the bias gradient
+    too, which runs beside the products; a replayed graph gives the same bits."""
+    monkeypatch.setenv("TP_BWD_CONCURRENT", concurrent)
+    T, h, f, p = 515, 256, 1024, 2
+    plan = _tp().Plan(h, f, 0, p, "bf16", "gelu")
+    plan.set_backward_defer(defer)
+    g = torch.Generator().manual_seed(5)
+    Z = [(torch.randn(T, f // p, generator=g) * 2).bfloat16() for _ in range(p)]
+    packed = [_encode(z.float(), "gelu") for z in Z]
+    Zq, Zs = [dev(q.view(torch.uint8)) for q, _ in packed], [dev(s) for _, s in packed]
+    dY = dev(torch.randn(T, h, generator=g).bfloat16())
+    W = [dev((torch.randn(h, f // p, generator=g) * 0.05).bfloat16()) for _ in range(p)]
+    new = lambda: ([torch.zeros(T, f // p, dtype=torch.bfloat16, device="cuda") for _ in range(p)],  # noqa: E731
+                   [torch.zeros(T, f // p, dtype=torch.bfloat16, device="cuda") for _ in range(p)],
+                   [torch.zeros(h, f // p, dtype=torch.bfloat16, device="cuda") for _ in range(p)], torch.zeros(h, device="cuda"))
+    flat = lambda o: [*o[0], *o[1], *o[2], o[3]]  # noqa: E731
+    first, side, graphed = new(), new(), new()
+    plan.row_bwd_ckpt8(T, dY, W, Zq, Zs, *first)
+    want = [host(t).copy() for t in flat(first)]
+    db = dY.double().sum(0).cpu().numpy()
+    bound = T * EPS * dY.double().abs().sum(0).cpu().numpy()
+    assert np.all(np.abs(want[-1] - db) <= bound)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        plan.row_bwd_ckpt8(T, dY, W, Zq, Zs, *side)
+        copies = [t.clone() for t in flat(side)]
+    st.synchronize()
+    assert all(np.array_equal(host(a), b) for a, b in zip(copies, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.row_bwd_ckpt8(T, dY, W, Zq, Zs, *graphed)
+    for _ in range(2):
+        for t in flat(graphed):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(host(a), b) for a, b in zip(flat(graphed), want))
+    assert _tp().device_status() == "TP_OK"
