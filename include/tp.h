@@ -329,7 +329,9 @@ TP_API tp_status tp_vocab_cross_entropy(tp_plan* plan, int64_t T, const void* co
  *   vocab entry, plus, when T > chunk and dW is wanted, fp32 sums of dW. Without
  *   gradients only per-row statistics of the score tiles are kept.
  * With T = 0, dW is set to zero. The workspace belongs to the plan and grows on
- * demand: make a call of the same sizes before capturing one. */
+ * demand: make a call of the same sizes before capturing one. fp32 plans compute dW
+ * beside dX on the device's side stream, which `stream` waits for before the call
+ * returns. */
 TP_API tp_status tp_vocab_linear_cross_entropy(tp_plan* plan, int64_t T, const void* X, const void* const* W,
                                                const int32_t* labels, float grad_scale, float* loss,
                                                float* lse, void* dX, void* const* dW, int64_t chunk,

@@ -409,40 +409,46 @@ bool side_stream_on() {
   return !(e && e[0] == '0');
 }
 
+}  // namespace
+
+namespace tpi {
+
+SideFork::SideFork(cudaStream_t st, bool on) : st_(st), s_(st) {
+  if (!on) return;
+  SideStream* sd = nullptr;
+  status_ = side_stream(&sd);
+  if (status_ == TP_OK) status_ = cuda_status(cudaEventRecord(sd->fork, st), "cudaEventRecord(fork)");
+  if (status_ == TP_OK) status_ = cuda_status(cudaStreamWaitEvent(sd->s, sd->fork, 0), "cudaStreamWaitEvent(fork)");
+  if (status_ != TP_OK) return;
+  s_ = sd->s;
+  join_ = sd->join;
+}
+
+SideFork::~SideFork() {
+  if (!join_) return;
+  if (cudaEventRecord(join_, s_) == cudaSuccess) cudaStreamWaitEvent(st_, join_, 0);
+  else cudaStreamSynchronize(s_);  // cannot join by event: finish the side work now
+  cudaGetLastError();
+}
+
+bool side_free(const tp_plan* plan) { return side_stream_on() && !plan->defer_bwd; }
+
+}  // namespace tpi
+
+namespace {
+
 bool concurrent_bwd(const tp_plan* plan, const GemmBatch& act_grad, const GemmBatch& wgrad) {
   if (plan->dtype != TP_BF16 || !side_stream_on()) return false;
   return !gemm_fills_gpu(act_grad) || !gemm_fills_gpu(wgrad);
 }
 
-// Runs `act_grad` on the side stream (forked from st); more work may follow
-// it there (stream()). When it goes out of scope, st waits for everything
-// issued on the side stream: every return path of the call joins.
-class SideGemm {
+// Runs `act_grad` on the side stream (forked from st); more work may follow it there.
+class SideGemm : public SideFork {
  public:
-  explicit SideGemm(cudaStream_t st) : st_(st) {  // the fork alone
-    status_ = side_stream(&sd_);
+  SideGemm(const tp_plan* plan, const GemmBatch& act_grad, cudaStream_t st) : SideFork(st) {
     if (status_ != TP_OK) return;
-    status_ = cuda_status(cudaEventRecord(sd_->fork, st), "cudaEventRecord(fork)");
-    if (status_ == TP_OK) status_ = cuda_status(cudaStreamWaitEvent(sd_->s, sd_->fork, 0), "cudaStreamWaitEvent(fork)");
-    if (status_ != TP_OK) sd_ = nullptr;
+    status_ = plan->dtype == TP_BF16 ? launch_gemm_bf16(act_grad, s_) : launch_gemm_f32(act_grad, s_);
   }
-  SideGemm(const tp_plan* plan, const GemmBatch& act_grad, cudaStream_t st) : SideGemm(st) {
-    if (status_ != TP_OK) return;
-    status_ = plan->dtype == TP_BF16 ? launch_gemm_bf16(act_grad, sd_->s) : launch_gemm_f32(act_grad, sd_->s);
-  }
-  ~SideGemm() {
-    if (!sd_) return;
-    if (cudaEventRecord(sd_->join, sd_->s) == cudaSuccess) cudaStreamWaitEvent(st_, sd_->join, 0);
-    else cudaStreamSynchronize(sd_->s);  // cannot join by event: finish the side work now
-    cudaGetLastError();
-  }
-  tp_status status() const { return status_; }
-  cudaStream_t stream() const { return sd_ ? sd_->s : st_; }
-
- private:
-  SideStream* sd_ = nullptr;
-  cudaStream_t st_;
-  tp_status status_ = TP_OK;
 };
 
 // Launch grouped GEMMs in the plan dtype; fp32 takes EPI_STORE only.
@@ -1905,15 +1911,11 @@ tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void*
   const int s = dW ? gemm_split_k(w) : 1;
   void* part = nullptr;
   if (s > 1) TP_TRY(scratch(plan, static_cast<size_t>(s) * p * h * k * sizeof(float), st, &part));
-  // dbias, a sum over dY alone, beside the products (40 -> 37 us at 2011 x 512 x 2048);
-  // not where weight gradients wait on the side stream, which the join would wait for
-  std::unique_ptr<SideGemm> side;
-  if (dbias && side_stream_on() && !plan->defer_bwd) {
-    side.reset(new SideGemm(st));
-    TP_TRY(side->status());
-  }
+  // dbias, a sum over dY alone, beside the products (40 -> 37 us at 2011 x 512 x 2048)
+  const SideFork side(st, dbias && side_free(plan));
+  TP_TRY(side.status());
   TP_TRY(launch_gemm_bf16(b, st));
-  if (dbias) TP_TRY(launch_column_sum(plan, dY, T, h, h, dbias, 0, plan->dtype, side ? side->stream() : st));
+  if (dbias) TP_TRY(launch_column_sum(plan, dY, T, h, h, dbias, 0, plan->dtype, side.stream()));
   if (!dW) return TP_OK;
   return s > 1 ? launch_gemm_split(w, s, static_cast<float*>(part), st) : launch_gemm_bf16(w, st);
 }

@@ -187,6 +187,27 @@ tp_status launch_vocab_ce(const PtrArray& L, const MutPtrArray& G, int p, int64_
                           const int32_t* labels, float scale, float* loss, float* lse, int64_t T,
                           tp_dtype dt, cudaStream_t st);
 
+// Work of a call beside that on its stream `st`: stream() is the device's side
+// stream, which waits for st, or st itself when not `on`. When the fork goes out of
+// scope, st waits for everything issued on the side stream: every return path of the
+// call joins. side_free: the side stream may be used so (it is not switched off, and
+// no deferred weight gradients of the plan are on it, which the join would wait for).
+class SideFork {
+ public:
+  explicit SideFork(cudaStream_t st, bool on = true);
+  ~SideFork();
+  SideFork(const SideFork&) = delete;
+  SideFork& operator=(const SideFork&) = delete;
+  tp_status status() const { return status_; }
+  cudaStream_t stream() const { return s_; }
+
+ protected:
+  cudaStream_t st_, s_;
+  cudaEvent_t join_ = nullptr;
+  tp_status status_ = TP_OK;
+};
+bool side_free(const tp_plan* plan);
+
 // Output head and cross-entropy without the logits (tp_loss.cu).
 tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const PtrArray& W,
                                  const int32_t* labels, float scale, float* loss, float* lse, void* dX,

@@ -261,3 +261,42 @@ def test_the_scale_is_not_rounded_with_d(T, chunk):
     rx = _reference(X, W, labels, V, scale)[2]
     err = float((torch.from_numpy(host(out[2])) - rx).norm() / rx.norm())
     assert err < 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -11 + 2.0 ** -8 / 100
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("chunk", [0, 100])
+def test_streams_and_replays_agree(dtype, chunk, monkeypatch):
+    """With and without the side stream, on another stream and replayed: the same bits, ready on
+    the caller's stream."""
+    plan, Vp, X, W, labels = _head(257, 128, 2003, 2, dtype, seed=21)
+    Xd, Ws, ld = dev(X), [dev(w) for w in W.chunk(2)], labels.cuda()
+
+    def new():
+        return torch.zeros(257, device="cuda"), torch.zeros_like(Xd), [torch.zeros_like(w) for w in Ws]
+
+    def call(o):
+        plan.vocab_linear_cross_entropy(257, Xd, Ws, ld, 0.37, o[0], None, o[1], o[2], chunk)
+        return [o[0].clone(), o[1].clone(), *[w.clone() for w in o[2]]]
+
+    want = call(new())
+    _check(X, W, labels, 2003, 0.37, (want[0], None, want[1], want[2:]), dtype)
+    monkeypatch.setenv("TP_BWD_CONCURRENT", "0")
+    assert all(torch.equal(a, b) for a, b in zip(call(new()), want))
+    monkeypatch.delenv("TP_BWD_CONCURRENT")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = call(new())
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    o = new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(o)
+    for _ in range(2):
+        for t in (o[0], o[1], *o[2]):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert _tp().device_status() == "TP_OK"
