@@ -27,19 +27,35 @@ constexpr int kBK = 16;
 constexpr int kPad = 4;  // keeps 16-byte shared loads aligned, store conflicts two-way
 
 __device__ __forceinline__ const float* row_of(const RowBlocks& m, int r) {
-  const int b = r / m.rows;
+  const int b = r < m.rows ? 0 : r / m.rows;
   return m.p[b] + static_cast<int64_t>(r - b * m.rows) * m.ld;
 }
 
-// One 16-byte piece of an operand's [ROWS x kBK] tile into registers: piece i of
-// the tile is 4 values along the operand's contiguous dimension.
+// A thread's 16-byte piece i of an operand's [ROWS x kBK] tiles: 4 values along the
+// operand's contiguous dimension. A K-major piece stays in its row, so its address is
+// stepped; an MN-major one finds its row anew in each K block, which costs fewer
+// registers than stepping it (where the kernel has none left).
 template <int ROWS, bool MN>
-__device__ __forceinline__ float4 load_piece(const RowBlocks& m, int i, int r0, int rows, int k0, int k1) {
-  const int r = r0 + (MN ? i % (ROWS / 4) * 4 : i / (kBK / 4));
-  const int k = k0 + (MN ? i / (ROWS / 4) : i % (kBK / 4) * 4);
-  if (r >= rows || k >= k1) return make_float4(0.f, 0.f, 0.f, 0.f);
-  return *reinterpret_cast<const float4*>(MN ? row_of(m, k) + r : row_of(m, r) + k);
-}
+struct Piece {
+  const float* p;
+  int k;  // its index in K; far past the end for rows the matrix does not have
+  __device__ __forceinline__ void start(const RowBlocks& m, int i, int r0, int rows, int k0) {
+    const int r = r0 + (MN ? i % (ROWS / 4) * 4 : i / (kBK / 4));
+    k = k0 + (MN ? i / (ROWS / 4) : i % (kBK / 4) * 4);
+    if (r >= rows) k = 1 << 30;
+    p = nullptr;
+    if constexpr (!MN) {
+      if (r < rows) p = row_of(m, r) + k;
+    }
+  }
+  __device__ __forceinline__ float4 next(const RowBlocks& m, int i, int r0, int k1) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < k1) v = *reinterpret_cast<const float4*>(MN ? row_of(m, k) + (r0 + i % (ROWS / 4) * 4) : p);
+    k += kBK;
+    if constexpr (!MN) p += kBK;
+    return v;
+  }
+};
 template <int ROWS, bool MN>
 __device__ __forceinline__ void store_piece(float (*s)[ROWS + kPad], int i, const float4& v) {
   if constexpr (MN) {
@@ -73,12 +89,18 @@ __global__ void __launch_bounds__(256, 2) fma_gemm_kernel(const __grid_constant_
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
 
   float4 ra[ALOADS], rb[BLOADS];
-  auto load = [&](int kb) {
+  Piece<BM, A_MN> pa[ALOADS];
+  Piece<kBN, B_MN> pb[BLOADS];
+#pragma unroll
+  for (int l = 0; l < ALOADS; ++l) pa[l].start(g.A, tid + l * 256, m0, g.M, k0);
+#pragma unroll
+  for (int l = 0; l < BLOADS; ++l) pb[l].start(g.B, tid + l * 256, n0, g.N, k0);
+  auto load = [&]() {
 #pragma unroll
     for (int l = 0; l < ALOADS; ++l)
-      if (APIECES % 256 == 0 || tid + l * 256 < APIECES) ra[l] = load_piece<BM, A_MN>(g.A, tid + l * 256, m0, g.M, kb, k1);
+      if (APIECES % 256 == 0 || tid + l * 256 < APIECES) ra[l] = pa[l].next(g.A, tid + l * 256, m0, k1);
 #pragma unroll
-    for (int l = 0; l < BLOADS; ++l) rb[l] = load_piece<kBN, B_MN>(g.B, tid + l * 256, n0, g.N, kb, k1);
+    for (int l = 0; l < BLOADS; ++l) rb[l] = pb[l].next(g.B, tid + l * 256, n0, k1);
   };
   auto store = [&](int buf) {
 #pragma unroll
@@ -87,12 +109,12 @@ __global__ void __launch_bounds__(256, 2) fma_gemm_kernel(const __grid_constant_
 #pragma unroll
     for (int l = 0; l < BLOADS; ++l) store_piece<kBN, B_MN>(sB[buf], tid + l * 256, rb[l]);
   };
-  load(k0);
+  load();
   store(0);
   __syncthreads();
   int buf = 0;
   for (int kb = k0; kb < k1; kb += kBK) {
-    if (kb + kBK < k1) load(kb + kBK);
+    if (kb + kBK < k1) load();
 #pragma unroll
     for (int k = 0; k < kBK; ++k) {
       float a[TM], b[8];
