@@ -199,7 +199,11 @@ tp_status launch_fma_gemm(const FmaGemm& g, float* part, cudaStream_t st) {
   const Shape s = shape_of(g);
   float* p = s.splits > 1 ? part : nullptr;
   const dim3 grid(static_cast<unsigned>(s.tiles), static_cast<unsigned>(s.splits));
-#define TP_FMA(TM, AM, BM) (void)launch(fma_gemm_kernel<TM, AM, BM>, grid, dim3(256), 0, st, g, s.tiles_n, s.k_split, p)
+  // Two kernels that follow a fork of streams overlap only when neither is launched
+  // programmatically: with the attribute the second began after the first had ended
+  // (launched one by one, 2048 x 16000 x 512 took 2583 us in place of 2338).
+  const bool early = pdl_enabled() && !g.beside;
+#define TP_FMA(TM, AM, BM) (void)launch_as(early, fma_gemm_kernel<TM, AM, BM>, grid, dim3(256), 0, st, g, s.tiles_n, s.k_split, p)
 #define TP_FMA_TM(AM, BM)                 \
   do {                                    \
     if (s.tm == 2) TP_FMA(2, AM, BM);     \

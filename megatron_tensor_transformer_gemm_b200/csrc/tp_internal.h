@@ -70,11 +70,11 @@ namespace tpi {
 // On unless the environment variable TP_PDL is "0".
 bool pdl_enabled();
 
-// Launch `kernel` on `st` with the programmatic-serialization attribute (when
-// enabled). Launch errors surface through cudaGetLastError as with <<<>>>.
+// Launch `kernel` on `st`, with the programmatic-serialization attribute if `early`.
+// Launch errors surface through cudaGetLastError as with <<<>>>.
 template <typename... Exp, typename... Act>
-inline cudaError_t launch(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                          Act&&... args) {
+inline cudaError_t launch_as(bool early, void (*kernel)(Exp...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                             Act&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -84,8 +84,14 @@ inline cudaError_t launch(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Act&&>(args)...);
+}
+// With the attribute when enabled.
+template <typename... Exp, typename... Act>
+inline cudaError_t launch(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                          Act&&... args) {
+  return launch_as(pdl_enabled(), kernel, grid, block, smem, st, static_cast<Act&&>(args)...);
 }
 
 // Record `fmt` as this thread's last error and return `s`.
@@ -362,6 +368,7 @@ struct FmaGemm {
   int M, N, K;
   RowBlocks A, B, D;
   bool a_mn, b_mn, add;
+  bool beside;  // runs beside another stream's kernel: see launch_fma_gemm
 };
 size_t fma_gemm_scratch(const FmaGemm& g);  // bytes of `part`
 tp_status launch_fma_gemm(const FmaGemm& g, float* part, cudaStream_t st);

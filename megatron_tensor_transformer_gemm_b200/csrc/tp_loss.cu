@@ -240,23 +240,23 @@ static tp_status linear_ce_f32(tp_plan* plan, int64_t T, const float* X, const P
     return m;
   };
   auto scores = [&](float* z, int64_t t0, int64_t n) {
-    return FmaGemm{static_cast<int>(n), Vp, h, plain(X + t0 * h, h), shards(W.p), plain(z, Vp), false, false, false};
+    return FmaGemm{static_cast<int>(n), Vp, h, plain(X + t0 * h, h), shards(W.p), plain(z, Vp), false, false, false, false};
   };
+  // The gradients' products beside one another, the one's tiles filling the other's
+  // last wave: 2048 x 16000 x 512 2583 -> 2338 us, 256 x 4000 x 256 135 -> 85, 500 x
+  // 8201 x 512 357 -> 350, 2 x 1000 x 64 25 either way. Not bf16's, which take turns on whole SMs: 500 x 5003 x 1024
+  // 54 -> 61 us.
+  const bool both = dX && dw && side_free(plan);
   auto dx_gemm = [&](float* d, int64_t t0, int64_t n) {
-    FmaGemm g{static_cast<int>(n), h, Vp, plain(d, Vp), shards(W.p), plain(dX + t0 * h, h), false, true, false};
+    FmaGemm g{static_cast<int>(n), h, Vp, plain(d, Vp), shards(W.p), plain(dX + t0 * h, h), false, true, false, both};
     g.D.rows = g.M;
     return g;
   };
   auto dw_gemm = [&](float* d, int64_t t0, int64_t n) {
     return FmaGemm{Vp, h, static_cast<int>(n), plain(d, Vp), plain(X + t0 * h, h),
-                   shards(const_cast<const void* const*>(dW.p)), true, true, t0 > 0};
+                   shards(const_cast<const void* const*>(dW.p)), true, true, t0 > 0, both};
   };
   const size_t z_bytes = round256(static_cast<size_t>(Tc) * Vp * 4);
-  // The gradients' products beside one another, the one's tiles filling the other's
-  // last wave: in a captured graph 2048 x 16000 x 512 2701 -> 2481 us, 652 x 2549 x 256
-  // 126 -> 110, 500 x 8201 x 512 375 -> 368 (launched one by one 377 either way). Not
-  // bf16's, which take turns on whole SMs: 500 x 5003 x 1024 54 -> 61 us.
-  const bool both = dX && dw && side_free(plan);
   size_t part_bytes = 0, w_bytes = 0;  // over the first (longest) and the last chunk
   for (int64_t t0 : {static_cast<int64_t>(0), (nch - 1) * Tc}) {
     const int64_t n = std::min(Tc, T - t0);
