@@ -243,8 +243,8 @@ static tp_status linear_ce_f32(tp_plan* plan, int64_t T, const float* X, const P
     return FmaGemm{static_cast<int>(n), Vp, h, plain(X + t0 * h, h), shards(W.p), plain(z, Vp), false, false, false, false};
   };
   // The gradients' products beside one another, the one's tiles filling the other's
-  // last wave: 2048 x 16000 x 512 2583 -> 2338 us, 256 x 4000 x 256 135 -> 85, 500 x
-  // 8201 x 512 357 -> 350, 2 x 1000 x 64 25 either way. Not bf16's, which take turns on whole SMs: 500 x 5003 x 1024
+  // last wave: 2048 x 16000 x 512 2326 -> 2072 us, 256 x 4000 x 256 124 -> 75, 500 x
+  // 8201 x 512 326 -> 318, 2 x 1000 x 64 25 either way. Not bf16's, which take turns on whole SMs: 500 x 5003 x 1024
   // 54 -> 61 us.
   const bool both = dX && dw && side_free(plan);
   auto dx_gemm = [&](float* d, int64_t t0, int64_t n) {
