@@ -404,6 +404,16 @@ tp_status side_stream(SideStream** out) {
   return TP_OK;
 }
 
+// The side stream waits for st. One event serves every call on the device, so the
+// record and the wait on it are one step for the host's threads: between them another
+// thread's record would make the side stream wait for that thread's stream instead.
+tp_status side_wait(SideStream* sd, cudaStream_t st) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  TP_TRY(cuda_status(cudaEventRecord(sd->fork, st), "cudaEventRecord(fork)"));
+  return cuda_status(cudaStreamWaitEvent(sd->s, sd->fork, 0), "cudaStreamWaitEvent(fork)");
+}
+
 bool side_stream_on() {
   const char* e = getenv("TP_BWD_CONCURRENT");
   return !(e && e[0] == '0');
@@ -417,8 +427,7 @@ SideFork::SideFork(cudaStream_t st, bool on) : st_(st), s_(st) {
   if (!on) return;
   SideStream* sd = nullptr;
   status_ = side_stream(&sd);
-  if (status_ == TP_OK) status_ = cuda_status(cudaEventRecord(sd->fork, st), "cudaEventRecord(fork)");
-  if (status_ == TP_OK) status_ = cuda_status(cudaStreamWaitEvent(sd->s, sd->fork, 0), "cudaStreamWaitEvent(fork)");
+  if (status_ == TP_OK) status_ = side_wait(sd, st);
   if (status_ != TP_OK) return;
   s_ = sd->s;
   join_ = sd->join;
@@ -1639,8 +1648,7 @@ tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void* dY,
     TP_TRY(flush_wgrad(plan));
     SideStream* sd = nullptr;
     TP_TRY(side_stream(&sd));
-    TP_TRY(cuda_status(cudaEventRecord(sd->fork, st), "cudaEventRecord(fork)"));
-    TP_TRY(cuda_status(cudaStreamWaitEvent(sd->s, sd->fork, 0), "cudaStreamWaitEvent(fork)"));
+    TP_TRY(side_wait(sd, st));
     TP_TRY(run_gemm(plan, b, st));
     if (dW) TP_TRY(launch_gemm_bf16(w, sd->s));
     if (dbias) {
@@ -1754,8 +1762,7 @@ static tp_status column_bwd_common(tp_plan* plan, tp_which which, int64_t T, con
     TP_TRY(flush_wgrad(plan));
     SideStream* sd = nullptr;
     TP_TRY(side_stream(&sd));
-    TP_TRY(cuda_status(cudaEventRecord(sd->fork, st), "cudaEventRecord(fork)"));
-    TP_TRY(cuda_status(cudaStreamWaitEvent(sd->s, sd->fork, 0), "cudaStreamWaitEvent(fork)"));
+    TP_TRY(side_wait(sd, st));
     if (has_dx) TP_TRY(run_gemm(plan, d, st));
     if (dW) TP_TRY(launch_gemm_bf16(w, sd->s));
     if (dbias)

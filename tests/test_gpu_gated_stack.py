@@ -192,3 +192,63 @@ def test_scoring_without_gradients():
     s = u.double() @ Wv.double().T
     ref = (torch.logsumexp(s, 1) - s.gather(1, labels.long().clamp(min=0)[:, None])[:, 0]) * (labels >= 0)
     assert head.dX is None and np.abs(host(loss) - ref.numpy()).max() <= 1e-3
+
+
+def test_two_threads_at_once():
+    """Two host threads, each with plans and a stream of its own, through the calls that share the
+    device's side stream: the bits of the same calls made one after the other."""
+    import threading
+
+    from megatron_tensor_transformer_gemm_b200 import tp
+    T, h, V, f = 300, 128, 2003, 512
+    n = 30
+
+    def make(seed):
+        g = torch.Generator().manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        head, mlp = tp.Plan(h, 0, 0, 1, "f32", "none"), tp.Plan(h, f, 0, 1, "bf16", "gelu")
+        Vp = head.set_vocab(V)
+        s = {"X": rnd(n, T, h).cuda(), "W": [(rnd(Vp, h) * 0.1).cuda()], "labels": torch.randint(0, V, (T,), generator=g, dtype=torch.int32).cuda(),
+             "dY": rnd(n, T, h).bfloat16().cuda(), "W2": [(rnd(h, f) * 0.05).bfloat16().cuda()], "Wc": [rnd(f, h).bfloat16().cuda()]}
+        return head, mlp, s
+
+    def run(head, mlp, s, out):
+        X16 = s["X"].bfloat16()
+        codes, scales = mlp.ckpt8_shapes(T)
+        e = lambda *z, dt=torch.float32: torch.empty(*z, dtype=dt, device="cuda")  # noqa: E731
+        bf = torch.bfloat16
+        for i in range(n):
+            loss, dX, dW = e(T), e(T, h), [torch.empty_like(s["W"][0])]
+            head.vocab_linear_cross_entropy(T, s["X"][i], s["W"], s["labels"], 0.5, loss, None, dX, dW)
+            Zq, Zs, H = [e(*codes, dt=torch.uint8)], [e(*scales, dt=torch.uint8)], [e(T, f, dt=bf)]
+            dZ, dW2, db = [e(T, f, dt=bf)], [e(h, f, dt=bf)], e(h)
+            mlp.column_fwd_ckpt8(T, X16[i], s["Wc"], None, Zq, Zs, H)
+            mlp.row_bwd_ckpt8(T, s["dY"][i], s["W2"], Zq, Zs, H, dZ, dW2, db)
+            out.append([loss, dX, dW[0], dZ[0], dW2[0], db])
+
+    sides = [make(31), make(32)]
+    want = [[], []]
+    for side, w in zip(sides, want):
+        run(*side, w)
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def thread(k):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                run(*sides[k], got[k])
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for w, g in zip(want, got):
+        for a, b in zip(w, g):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert tp.device_status() == "TP_OK"
