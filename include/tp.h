@@ -321,8 +321,8 @@ TP_API tp_status tp_vocab_cross_entropy(tp_plan* plan, int64_t T, const void* co
  *   target score (0 for ignored tokens); lse [T] fp32 (NULL ok).
  *   dX [T, hidden] (NULL skips) = grad_scale * sum_i d_i W[i] and dW[i] [Vp/p,
  *   hidden] (NULL array skips) = grad_scale * d_i^T X, with d = softmax - onehot
- *   rounded to the plan dtype before the two products; sums are fp32 and rounded
- *   once, scaled.
+ *   rounded to the plan dtype before the two products (in bf16 chunks of at most 64
+ *   tokens held in two bf16 parts); sums are fp32 and rounded once, scaled.
  *   Padding rows of dW are zero. dX and dW must not alias X and W.
  *   chunk: tokens whose scores are worked on at a time (0: the library's choice);
  *   the workspace holds them as 2 (bf16) or 4 (fp32) bytes per token and padded

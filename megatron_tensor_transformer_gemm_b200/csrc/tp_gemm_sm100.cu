@@ -2035,7 +2035,7 @@ GemmBatch cat_parts(const GemmBatch& b, int parts) {
 }
 }  // namespace
 
-int gemm_cat_split(const GemmBatch& b) {
+int gemm_cat_split(const GemmBatch& b, int most) {
   if (!b.kcat || b.scatter_n || b.epi != EPI_STORE || b.n < 1) return 1;
   for (int i = 0; i < b.n; ++i)
     if (b.g[i].K != b.g[0].K || b.g[i].bias || b.g[i].aux || b.g[i].acc) return 1;
@@ -2045,7 +2045,7 @@ int gemm_cat_split(const GemmBatch& b) {
   double best_cost = 0.0;
   choose_layout(b, sms, &best_cost);
   int best = 1;
-  for (int parts = 2; parts <= TP_MAX_SHARDS; ++parts) {
+  for (int parts = 2; parts <= most; ++parts) {
     if (parts < b.n ? b.n % parts : parts % b.n) continue;
     if (parts > b.n) {
       const int s = parts / b.n, kbps = (nkb + s - 1) / s;
@@ -2062,7 +2062,7 @@ int gemm_cat_split(const GemmBatch& b) {
   return best;
 }
 
-tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cudaStream_t st) {
+tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cudaStream_t st, int fold) {
   const int64_t M = b.g[0].M, N = b.g[0].N, mn = M * N;
   MutPtrArray out{};
   out.p[0] = b.g[0].D;
@@ -2075,8 +2075,8 @@ tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cuda
   tp_status r = launch_gemm_bf16(t, st);
   if (r != TP_OK) return r;
   PtrArray P{};
-  for (int j = 0; j < parts; ++j) P.p[j] = part + j * mn;
-  return launch_reduce(P, parts, nullptr, nullptr, PtrArray{}, false, out, false, 1, M, N, TP_F32, TP_BF16, st);
+  for (int j = 0; j < parts * fold; ++j) P.p[j] = part + j * (mn / fold);
+  return launch_reduce(P, parts * fold, nullptr, nullptr, PtrArray{}, false, out, false, 1, M / fold, N, TP_F32, TP_BF16, st);
 }
 
 }  // namespace tpi

@@ -348,9 +348,10 @@ tp_status launch_gemm_split(GemmBatch b, int s, float* part, cudaStream_t st);
 // `parts` fp32 partial sums (<= 16 of M * N floats in `part`: whole segments
 // together, or every segment split) and one ordered reduce. gemm_cat_split: the
 // parts that take least time by the estimate, 1 for b as it is; a last wave of
-// tiles that fills few SMs, or few tiles with a long K, gain from it.
-int gemm_cat_split(const GemmBatch& b);
-tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cudaStream_t st);
+// tiles that fills few SMs, or few tiles with a long K, gain from it. fold: the M rows
+// are that many blocks, which are added too (parts * fold <= 16).
+int gemm_cat_split(const GemmBatch& b, int most = TP_MAX_SHARDS);
+tp_status launch_gemm_cat_split(const GemmBatch& b, int parts, float* part, cudaStream_t st, int fold = 1);
 // fp32 FMA path (tp_gemm_simt.cu): the same epilogues, grouping and K concatenation.
 tp_status launch_gemm_f32(const GemmBatch& b, cudaStream_t st);
 

@@ -13,8 +13,8 @@
 // softmax, joined), adds the label's score, and turns the exponentials into d in
 // place with one factor 2^(m - lse2) per slot; then the two products, whose
 // epilogues apply the scale (in d's rounding to bf16 the labels' entries, all near
-// -scale, would share one error, up to 2^-9 of the gradients). So
-// each score is computed once: 6 T V h operations for loss and gradients, against
+// -scale, would share one error, up to 2^-8 of the gradients). So each score is
+// computed once: 6 T V h operations for loss and gradients, against
 // 8 for recomputing the scores in the backward, at 6 bytes of traffic per score.
 // fp32 plans keep the chunk's scores in fp32.
 // Bound by the tensor cores: 4096 x 131072 x 4096 over 8 shards in 10.6 ms, 1245
@@ -113,12 +113,13 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
 // The label's score is a dot product of its own, in fp32 by the CTA: the tensor
 // cores' long accumulation is less exact, and a confident token's loss is the
 // difference of lse and this score. gridDim.y CTAs share a row's second part
-// (few rows: the merge is short and repeated by each).
+// (few rows: the merge is short and repeated by each). lo_at != 0: d's rounding error,
+// in bf16 too, goes lo_at vectors behind d, and x2 receives X twice.
 constexpr int kFinThreads = 256;
 __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
     const float4* stats, int shard_pairs, const __nv_bfloat16* X,
     const __grid_constant__ PtrArray W, int h, int vocab, int Vs, int p, const int32_t* labels, float* loss,
-    float* lse_out, uint4* e, unsigned* status) {
+    float* lse_out, uint4* e, int64_t lo_at, uint4* x2, unsigned* status) {
   tpd::pdl_entry();
   __shared__ float2 red[kFinThreads / 32];
   __shared__ float dot[kFinThreads / 32];
@@ -165,12 +166,19 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
     if (lse_out) lse_out[t] = lse2 * kLn2;
   }
   if (!e) return;
+  if (x2 && blockIdx.y == 0) {  // X beside itself, for the two parts of d
+    const uint4* x = reinterpret_cast<const uint4*>(X + t * h);
+    for (int i = threadIdx.x; i < h / 8; i += kFinThreads) x2[t * (h / 8) + i] = x2[(t + gridDim.x) * (h / 8) + i] = x[i];
+  }
   const int nv = Vs / 8, total = p * nv;  // 16-byte vectors of the row
   uint4* row = e + t * total;
   const int per = (total + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
   const int lo = static_cast<int>(blockIdx.y) * per, hi = min(total, lo + per);
   if (ignore) {
-    for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) row[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) {
+      row[i] = make_uint4(0, 0, 0, 0);
+      if (lo_at) row[i + lo_at] = make_uint4(0, 0, 0, 0);
+    }
     return;
   }
   const float at_label = tpd::ex2(z2 - lse2) - 1.f;
@@ -194,8 +202,18 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
       for (int q = 0; q < 8; ++q)
         if (q == label % 8) d[q] = at_label;
     }
-    row[i] = make_uint4(tpd::pack_bf16x2(d[0], d[1]), tpd::pack_bf16x2(d[2], d[3]), tpd::pack_bf16x2(d[4], d[5]),
-                        tpd::pack_bf16x2(d[6], d[7]));
+    const uint32_t r[4] = {tpd::pack_bf16x2(d[0], d[1]), tpd::pack_bf16x2(d[2], d[3]), tpd::pack_bf16x2(d[4], d[5]),
+                           tpd::pack_bf16x2(d[6], d[7])};
+    row[i] = make_uint4(r[0], r[1], r[2], r[3]);
+    if (lo_at) {
+      uint32_t s[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 v = tpd::unpack_bf16x2(r[q]);
+        s[q] = tpd::pack_bf16x2(d[2 * q] - v.x, d[2 * q + 1] - v.y);
+      }
+      row[i + lo_at] = make_uint4(s[0], s[1], s[2], s[3]);
+    }
   }
 }
 
@@ -303,6 +321,12 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
   // without gradients, 8 bytes are kept per slot of 64 scores
   const int64_t Tc = pick_chunk(T, Vp, h, grad ? 2.0 : 0.125, dw, chunk);
   const int64_t nch = (T + Tc - 1) / Tc;
+  // Chunks of at most 64 tokens carry d in two bf16 parts, in 2n rows that still fit one
+  // tile row of dX and, up to 32 tokens, one K block of dW: with few tokens a row of the
+  // gradients has one or two large terms, whose rounding it would carry whole (relative
+  // errors up to 0.004 in place of the result's own 0.0017).
+  const bool two = grad && Tc <= 64;
+  const int fold = two ? 2 : 1;
 
   // products with d of a chunk of n tokens starting at token t0
   auto dx_batch = [&](const void* d, int64_t t0, int64_t n) {
@@ -315,7 +339,7 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     b.alpha = scale;
     for (int i = 0; i < p; ++i) {
       GemmProblem& g = b.g[i];
-      g.M = static_cast<int>(n);
+      g.M = static_cast<int>(fold * n);
       g.N = h;
       g.K = Vs;
       g.A = static_cast<const uint8_t*>(d) + static_cast<size_t>(i) * Vs * es;
@@ -327,6 +351,7 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     }
     return b;
   };
+  const void* x2 = nullptr;  // X twice, beside d's two parts
   auto dw_batch = [&](const void* d, int64_t t0, int64_t n) {
     GemmBatch b{};
     b.n = p;
@@ -338,10 +363,10 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
       GemmProblem& g = b.g[i];
       g.M = Vs;
       g.N = h;
-      g.K = static_cast<int>(n);
+      g.K = static_cast<int>(fold * n);
       g.A = static_cast<const uint8_t*>(d) + static_cast<size_t>(i) * Vs * es;
       g.lda = Vp;
-      g.B = static_cast<const uint8_t*>(X) + static_cast<size_t>(t0) * h * es;
+      g.B = two ? x2 : static_cast<const uint8_t*>(X) + static_cast<size_t>(t0) * h * es;
       g.ldb = h;
       g.D = dW.p[i];
       g.ldd = h;
@@ -373,18 +398,23 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
   const int shard_pairs = (Vs + 127) / 128;  // pairs of slots, see GemmBatch::ce_stats
 
   // scratch: d (from the exponentials or scores) | statistics | fp32 sums of dW | split-K partials
-  const int sx = dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc)) : 1;
+  const int sx = dX ? gemm_cat_split(dx_batch(nullptr, 0, Tc), TP_MAX_SHARDS / fold) : 1;
   const int sw = dw && nch == 1 ? gemm_split_k(dw_batch(nullptr, 0, Tc)) : 1;
-  const size_t d_bytes = grad ? round256(static_cast<size_t>(Tc) * Vp * es) : 0;
+  const size_t d_bytes = grad ? round256(static_cast<size_t>(fold * Tc) * Vp * es) : 0;
   const size_t st_bytes = round256(static_cast<size_t>(Tc) * p * shard_pairs * sizeof(float4));
   const size_t acc_bytes = dw && nch > 1 ? round256(static_cast<size_t>(Vp) * h * 4) : 0;
-  const size_t part_bytes = std::max(sx > 1 ? static_cast<size_t>(sx) * Tc * h * 4 : 0, sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0);
+  const bool x_parts = dX && (sx > 1 || two);
+  const size_t part_bytes = round256(std::max(x_parts ? static_cast<size_t>(sx) * fold * Tc * h * 4 : 0,
+                                              sw > 1 ? static_cast<size_t>(sw) * Vp * h * 4 : 0));
+  const size_t x2_bytes = two && dw ? static_cast<size_t>(2 * Tc) * h * es : 0;
   void* ws = nullptr;
-  TP_TRY(scratch(plan, d_bytes + st_bytes + acc_bytes + part_bytes, st, &ws));
+  TP_TRY(scratch(plan, d_bytes + st_bytes + acc_bytes + part_bytes + x2_bytes, st, &ws));
   uint8_t* db = static_cast<uint8_t*>(ws);
   float2* stats = reinterpret_cast<float2*>(db + d_bytes);
   float* acc = reinterpret_cast<float*>(db + d_bytes + st_bytes);
   float* part = reinterpret_cast<float*>(db + d_bytes + st_bytes + acc_bytes);
+  uint4* xx = x2_bytes ? reinterpret_cast<uint4*>(db + d_bytes + st_bytes + acc_bytes + part_bytes) : nullptr;
+  x2 = xx;
 
   for (int64_t c = 0; c < nch; ++c) {
     const int64_t t0 = c * Tc, n = std::min(Tc, T - t0);
@@ -397,11 +427,11 @@ tp_status launch_vocab_linear_ce(tp_plan* plan, int64_t T, const void* X, const 
     (void)launch(ce_finish_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(parts)), dim3(kFinThreads), 0, st,
                  reinterpret_cast<const float4*>(stats), shard_pairs, static_cast<const __nv_bfloat16*>(X) + t0 * h, W, h,
                  V, Vs, p, labels + t0, loss + t0, lse ? lse + t0 : nullptr,
-                 grad ? reinterpret_cast<uint4*>(db) : nullptr, status);
+                 grad ? reinterpret_cast<uint4*>(db) : nullptr, two ? n * (Vp / 8) : int64_t{0}, xx, status);
     TP_TRY(after_launch("vocab_linear_cross_entropy rows"));
     if (dX) {
       const GemmBatch x = dx_batch(db, t0, n);
-      if (sx > 1) TP_TRY(launch_gemm_cat_split(x, sx, part, st));
+      if (x_parts) TP_TRY(launch_gemm_cat_split(x, sx, part, st, fold));
       else TP_TRY(launch_gemm_bf16(x, st));
     }
     if (dw) {

@@ -300,3 +300,35 @@ def test_streams_and_replays_agree(dtype, chunk, monkeypatch):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert _tp().device_status() == "TP_OK"
+
+
+@pytest.mark.parametrize("T,V,p,chunk", [(1, 1003, 2, 0), (2, 40000, 8, 0), (17, 3001, 1, 0), (33, 259, 2, 0), (64, 5003, 4, 0),
+                                         (200, 1003, 2, 50), (65, 1003, 1, 64), (64, 131, 1, 63)])
+def test_few_tokens_carry_d_twice(T, V, p, chunk):
+    """Chunks of at most 64 tokens: d is held in two bf16 parts, off by 2^-8 of 2^-8 of it, so
+    what is left is the exponentials' 2^-10 of the softmax (the label's own entry is exact),
+    the fp32 sums and the result's rounding."""
+    plan, Vp, X, W, labels = _head(T, 128, V, p, "bf16", seed=T + p, std=0.3)
+    scale = 1.37 / T
+    loss, lse, dX, dW = _run(plan, Vp, X, W, labels, scale, chunk)
+    _check(X, W, labels, V, scale, (loss, lse, dX, dW), "bf16")
+    rl, rs, rx, rw, bx, bw, px, pw = _reference(X, W, labels, V, scale)
+    eps = 2.0 ** -24
+    z_err = 128 * eps * float((X.double().norm(dim=1) * W[:V].double().norm(dim=1).max()).max())
+    rel = z_err + 2.0 ** -21 + 4 * eps * float(rs.abs().max() + 8) + 2.0 ** -10
+    lab = labels.long().clamp(min=0)
+    keep = (labels >= 0).double()
+    pl = torch.exp((X.double() * W.double()[lab]).sum(1) - rs) * scale * keep  # the label's softmax: exact but for z
+    for got, ref, b, pr in ((host(dX), rx, bx, px), (np.concatenate([host(w) for w in dW]), rw, bw, pw)):
+        lim = (2.0 ** -16 + (V + T) * eps) * b + rel * pr + 2.0 ** -8 * ref.abs() + 1e-30
+        assert np.all(np.abs(got - ref.numpy()) <= lim.numpy())
+    # the label's row of a token that shares it with none has no 2^-10 either: beyond the
+    # result's rounding only the other tokens' softmax in it
+    one = [t for t in range(T) if keep[t] > 0 and int((lab == lab[t]).sum()) == 1]
+    got = torch.from_numpy(np.concatenate([host(w) for w in dW]))
+    for t in one:
+        v = int(lab[t])
+        others = pw[v] - pl[t] * X[t].double().abs()
+        lim = (2.0 ** -16 + T * eps) * bw[v] + (rel - 2.0 ** -10) * pw[v] + 2.0 ** -10 * others.clamp(min=0) + 2.0 ** -8 * rw[v].abs() + 1e-30
+        assert bool(((got[v] - rw[v]).abs() <= lim * (1 + 1e-6)).all())
+    assert _tp().device_status() == "TP_OK"
