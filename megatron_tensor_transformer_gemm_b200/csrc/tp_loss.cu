@@ -5,13 +5,19 @@
 //   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label
 //   d_tv  = exp(z_tv - lse_t) - [v = label],  dX = scale * d W,  dW = scale * d^T X
 //
+// For a token whose label is all but certain both differences are small against what they
+// are taken of: lse or the softmax rounded to fp32 would leave few digits of them. So the
+// label stays out of the sum over the others, and with o their share and t the label's,
+// both relative to the larger of the two maxima, loss = log1p(o / t) and the label's d is
+// -o / (o + t), each good to a few roundings of its own size.
+//
 // Tokens are taken a chunk at a time. For bf16 plans the scores live only in the
 // tensor cores' fp32 accumulators: the GEMM's epilogue leaves, per row and slot of
 // 64 columns, their maximum m and sum of 2^(z log2 e - m), and, when
 // gradients are wanted, the exponentials themselves in 16 bits (relative to the
 // slot's maximum). A row kernel merges the slots (the running maximum and sum of a
 // softmax, joined), adds the label's score, and turns the exponentials into d in
-// place with one factor 2^(m - lse2) per slot; then the two products, whose
+// place with one factor 2^(m - M) / (o + t) per slot; then the two products, whose
 // epilogues apply the scale (in d's rounding to bf16 the labels' entries, all near
 // -scale, would share one error, up to 2^-8 of the gradients). So each score is
 // computed once: 6 T V h operations for loss and gradients, against
@@ -44,6 +50,24 @@ __device__ __forceinline__ float2 merge(float2 a, float2 b) {
   return make_float2(m, a.y * tpd::ex2(a.x - m) + b.y * tpd::ex2(b.x - m));
 }
 
+// A row's softmax split into the label's share t and the others' o, both relative to 2^M.
+struct Split {
+  float M, o, t;
+  __device__ __forceinline__ float sum() const { return o + t; }
+  __device__ __forceinline__ float lse() const { return (M + log2f(sum())) * kLn2; }
+};
+// rest: (max, sum) of all columns but the label's, whose score is z (kept: a label that counts).
+// t is taken from z itself, so that M's own rounding is in both shares alike.
+__device__ __forceinline__ Split split_row(const float2& rest, bool kept, float z) {
+  if (!kept) return Split{rest.x, rest.y, 0.f};
+  const float M = fmaxf(rest.x, z * kLog2e);
+  return Split{M, rest.y * tpd::ex2(rest.x - M), tpd::ex2(fmaf(z, kLog2e, -M))};
+}
+__device__ __forceinline__ float row_loss(const Split& s, const float2& rest, float z) {
+  if (z * kLog2e >= rest.x) return log1pf(s.o / s.t);
+  return (fmaf(-z, kLog2e, s.M) + log2f(s.sum())) * kLn2;  // at least log 2: nothing cancels
+}
+
 template <int THREADS>
 __device__ __forceinline__ float2 block_merge(float2 v, float2* red) {
 #pragma unroll
@@ -70,6 +94,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
   const int label = labels[t];
   const bool ignore = label < 0 || label >= vocab;
   const float* row = z + t * ld;
+  const float zl = ignore ? 0.f : row[label];  // read before block_merge's barrier: d may be z
   float2 acc = make_float2(-INFINITY, 0.f);
   for (int c = threadIdx.x * 4; c < vocab; c += kRowThreads * 4) {
     const float4 u = *reinterpret_cast<const float4*>(row + c);
@@ -77,32 +102,34 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows_kernel(const float* z, in
     float m = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[e] = c + e < vocab ? x[e] * kLog2e : -INFINITY;
+      if (c + e >= vocab || c + e == label) x[e] = -INFINITY;
       m = fmaxf(m, x[e]);
     }
+    m *= kLog2e;
     const float mo = m == -INFINITY ? 0.f : m;
-    acc = merge(acc, make_float2(m, tpd::ex2(x[0] - mo) + tpd::ex2(x[1] - mo) + tpd::ex2(x[2] - mo) + tpd::ex2(x[3] - mo)));
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += tpd::ex2(fmaf(x[e], kLog2e, -mo));
+    acc = merge(acc, make_float2(m, sum));
   }
-  const float2 tot = block_merge<kRowThreads>(acc, red);
-  const float lse2 = tot.x + log2f(tot.y);
+  const float2 rest = block_merge<kRowThreads>(acc, red);
+  const Split s = split_row(rest, !ignore, zl);
   if (threadIdx.x == 0) {
     if (label >= vocab) atomicOr(status, kStatusBadIndex);
-    loss[t] = ignore ? 0.f : lse2 * kLn2 - row[label];
-    if (lse_out) lse_out[t] = lse2 * kLn2;
+    loss[t] = ignore ? 0.f : row_loss(s, rest, zl);
+    if (lse_out) lse_out[t] = s.lse();
   }
   if (!d) return;
-  __syncthreads();  // the label's score has been read: d may be z
   float* drow = d + t * ld;
+  const float k = scale / s.sum(), at_label = -(s.o / s.sum()) * scale;
   for (int64_t c = threadIdx.x * 4; c < ld; c += kRowThreads * 4) {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (!ignore && c < vocab) {
       const float4 u = *reinterpret_cast<const float4*>(row + c);
       x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float pr = c + e < vocab ? tpd::ex2(fmaf(x[e], kLog2e, -lse2)) : 0.f;
-        x[e] = (pr - (c + e == label ? 1.f : 0.f)) * scale;
-      }
+      for (int e = 0; e < 4; ++e)
+        x[e] = c + e == label ? at_label : c + e < vocab ? tpd::ex2(fmaf(x[e], kLog2e, -s.M)) * k : 0.f;
     }
     *reinterpret_cast<float4*>(drow + c) = make_float4(x[0], x[1], x[2], x[3]);
   }
@@ -153,17 +180,15 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   if ((threadIdx.x & 31) == 0) dot[threadIdx.x >> 5] = z;
-  float2 tot = block_merge<kFinThreads>(acc, red);  // its barrier covers dot
+  const float2 rest = block_merge<kFinThreads>(acc, red);  // its barrier covers dot
   z = 0.f;
 #pragma unroll
   for (int w = 0; w < kFinThreads / 32; ++w) z += dot[w];
-  const float z2 = z * kLog2e;
-  if (!ignore) tot = merge(tot, make_float2(z2, 1.f));
-  const float lse2 = tot.x + log2f(tot.y);
+  const Split sp = split_row(rest, !ignore, z);
   if (threadIdx.x == 0 && blockIdx.y == 0) {
     if (label >= vocab) atomicOr(status, kStatusBadIndex);
-    loss[t] = ignore ? 0.f : (tot.x - z2 + log2f(tot.y)) * kLn2;
-    if (lse_out) lse_out[t] = lse2 * kLn2;
+    loss[t] = ignore ? 0.f : row_loss(sp, rest, z);
+    if (lse_out) lse_out[t] = sp.lse();
   }
   if (!e) return;
   if (x2 && blockIdx.y == 0) {  // X beside itself, for the two parts of d
@@ -181,14 +206,14 @@ __global__ void __launch_bounds__(kFinThreads) ce_finish_kernel(
     }
     return;
   }
-  const float at_label = tpd::ex2(z2 - lse2) - 1.f;
+  const float inv = 1.f / sp.sum(), at_label = -(sp.o / sp.sum());
 #pragma unroll 4
   for (int i = lo + threadIdx.x; i < hi; i += kFinThreads) {
     const uint4 u = row[i];
     const int sh = i / nv, c = (i - sh * nv) * 8;
     const float4* at = st + sh * shard_pairs + c / 128;
     const float m = c & 64 ? at->z : at->x;  // -inf: all its exps are 0
-    const float f = tpd::ex2(m - lse2);
+    const float f = tpd::ex2(m - sp.M) * inv;
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     float d[8];
 #pragma unroll
