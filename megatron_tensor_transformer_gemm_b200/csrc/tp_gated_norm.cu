@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 32 * kWarpRows : THREADS) gate
 // sums are added in a fixed order by a second kernel.
 // Bound by HBM for RMSNorm: 8192 x 8192 bf16 with 8 gate rows and every sum 146 us,
 // 5.5 TB/s. LayerNorm has two sums more a column, whose registers leave half as many
-// rows in flight: 207 us, 3.9 TB/s; 32768 x 4096 353 us, 4.6. In fp32 2049 x 520
+// rows in flight: 202 us, 4.0 TB/s; 32768 x 4096 363 us, 4.4. In fp32 2049 x 520
 // takes 15 us: two launches and 512 CTAs' partial sums beside 26 MB of rows.
 constexpr int kStages = 3;
 
@@ -431,16 +431,17 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
   int turn = 0, s = 0;
   uint32_t phase = 0;
   int run = -1;  // gate row of the current run
-  // the row's statistics as xh = x * r + c
+  // The row's statistics as xh = (x + c) * r, c = -mean: the difference first. As x * r + c r,
+  // an instruction less, xh would be off by 2^-24 of mean * r however small it is itself.
   float r1 = 1.f, c1 = 0.f, r2 = 1.f, c2 = 0.f;
   auto load_stats = [&](int t) {
     if (post) {
       r1 = p.stats[p.rows + t];
-      if (!RMS) c1 = -p.stats[t] * r1;
+      if (!RMS) c1 = -p.stats[t];
     }
     if (pre) {
       r2 = p.stats[3 * p.rows + t];
-      if (!RMS) c2 = -p.stats[2 * p.rows + t] * r2;
+      if (!RMS) c2 = -p.stats[2 * p.rows + t];
     }
   };
   load_stats(at.t);  // every CTA has a row (G <= rows)
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
           Vec16<T>::unpack(g2[i], w);
 #pragma unroll
           for (int e = 0; e < N / 2; ++e) {
-            const uint64_t xh = RMS ? mul2(x[e], r) : fma2(x[e], r, k), gy = mul2(d[e], w[e]);
+            const uint64_t xh = mul2(RMS ? x[e] : tpd::add2(x[e], k), r), gy = mul2(d[e], w[e]);
             if (!RMS) mx = tpd::add2(mx, gy);
             my = fma2(gy, xh, my);
             P[i][e] = fma2(d[e], xh, P[i][e]);
@@ -511,9 +512,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
     if (!good) break;
     // every thread is past the row before this one: its stage takes a new row
     if (threadIdx.x == 0 && left < count && to_issue > 0) issue();
-    // D = dx_out + R2 (gy - m1 - xh m2), with xh = x R2 + C2 folded into x's factor
+    // D = dx_out + R2 (gy - m1 - xh m2), xh = (x + C2) R2
     const float m1 = m.x * inv_h, m2 = m.y * inv_h;
-    const uint64_t fx = both(-R2 * m2 * R2), f0 = both(-R2 * fmaf(C2, m2, m1)), fr = both(R2), rs = both(p.rs);
+    const uint64_t fx = both(-R2 * m2 * R2), f0 = both(-R2 * m1), fr = both(R2), rs = both(p.rs), c2v = both(C2);
     const uint64_t r1v = both(R1), c1v = both(C1);
     const uint32_t at_a = pre ? s_x : s_a;
     uint64_t ux = 0, uy = 0;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
           const uint64_t v = RMS ? D[e] : tpd::add2(D[e], f0);
-          D[e] = fma2(x[e], fx, fma2(mul2(d[e], w[e]), fr, v));
+          D[e] = fma2(RMS ? x[e] : tpd::add2(x[e], c2v), fx, fma2(mul2(d[e], w[e]), fr, v));
         }
       }
 #pragma unroll
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
         unpack_shared<T>(s_f + c * 16, x);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
-          x[e] = RMS ? mul2(x[e], r1v) : fma2(x[e], r1v, c1v);
+          x[e] = mul2(RMS ? x[e] : tpd::add2(x[e], c1v), r1v);
           A[i][e] = fma2(D[e], x[e], A[i][e]);
           if (!RMS) S[i][e] = tpd::add2(S[i][e], D[e]);
         }
@@ -571,10 +572,10 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
     if (post) {
       float2 u = make_float2(RMS ? 0.f : sum2(ux), sum2(uy));
       good = pair_sum<MAXT, CL>(u, true, red, turn, rank);
-      // df = R1 (a - u1 - xh u2), xh = f R1 + C1
+      // df = R1 (a - u1 - xh u2), xh = (f + C1) R1
       const float u1 = u.x * inv_h, u2 = u.y * inv_h;
       fu = both(-R1 * u2 * R1);
-      fc = both(RMS ? 0.f : -R1 * fmaf(C1, u2, u1));
+      fc = both(RMS ? 0.f : -R1 * u1);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 512 / MAXT : 1) gated_norm
         unpack_shared<T>(s_f + c * 16, x);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e)
-          o[e] = fma2(x[e], fu, RMS ? mul2(o[e], r1v) : fma2(o[e], r1v, fc));
+          o[e] = fma2(RMS ? x[e] : tpd::add2(x[e], c1v), fu, RMS ? mul2(o[e], r1v) : fma2(o[e], r1v, fc));
       }
       reinterpret_cast<uint4*>(static_cast<T*>(p.df) + row_at)[c] = Vec16<T>::pack(o);
     }
