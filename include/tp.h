@@ -36,7 +36,10 @@
  *     asynchronous on it; they take no locks and never synchronise.
  *   - Ownership: the caller owns every tensor. The plan owns host metadata and
  *     a device workspace that the library allocates (cudaMalloc) the first
- *     time a call needs scratch space and frees in tp_plan_destroy.
+ *     time a call needs scratch space, replaces by a larger one when a call needs
+ *     more, and frees in tp_plan_destroy. A workspace that a call in a stream
+ *     capture was given stays until then, since graphs replay with its address:
+ *     destroy a plan after the graphs captured from it.
  *   - Errors: argument, shape, divisibility and alignment errors are detected
  *     on the host and returned BEFORE any launch, with detail text available
  *     from tp_last_error() (thread-local). A failed launch returns TP_ERR_CUDA.

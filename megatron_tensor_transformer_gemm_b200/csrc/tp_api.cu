@@ -132,138 +132,102 @@ tp_status device_status_word(unsigned** out) {
   return TP_OK;
 }
 
-void note_capture(tp_plan* plan, cudaStream_t st) {
+static bool capturing(cudaStream_t st) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
+  if (cudaStreamIsCapturing(st, &cs) == cudaSuccess) return cs != cudaStreamCaptureStatusNone;
+  cudaGetLastError();
+  return false;
+}
+
+// Let go of a block that another one replaces: freed once the device's work is done, or
+// kept until the plan is destroyed when a graph may replay with its address, and where
+// the device cannot be waited for now (in a capture).
+static tp_status release_block(tp_plan* plan, Block& b, int cur, bool in_capture) {
+  if (!b.p) return TP_OK;
+  if (!b.held && !in_capture) {
+    if (b.device != cur) cudaSetDevice(b.device);
+    const bool freed = cudaDeviceSynchronize() == cudaSuccess && cudaFree(b.p) == cudaSuccess;
     cudaGetLastError();
-    return;
-  }
-  if (cs != cudaStreamCaptureStatusNone) plan->captured = 1;
-}
-
-// Let go of a workspace block that a larger one replaces: freed once the
-// device's work is done, or, when graphs captured from this plan may replay
-// with its address, kept until the plan is destroyed.
-static tp_status release_block(tp_plan* plan, void* p, int device, int cur) {
-  if (plan->captured) {
-    Retired* r = new (std::nothrow) Retired{p, device, plan->retired};
-    if (!r) return fail(TP_ERR_ARG, "out of host memory for the plan's workspace");
-    plan->retired = r;
-    return TP_OK;
-  }
-  if (device != cur) cudaSetDevice(device);
-  cudaDeviceSynchronize();
-  cudaFree(p);
-  if (device != cur) cudaSetDevice(cur);
-  return TP_OK;
-}
-
-tp_status workspace(tp_plan* plan, size_t bytes, void** out) {
-  int dev = 0;
-  tp_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
-  if (s != TP_OK) return s;
-  if (plan->ws && (plan->ws_bytes < bytes || plan->ws_device != dev)) {
-    // Grow (or move to another device): release the old block first. The
-    // caller's stream may still use it, so wait for the device.
-    TP_TRY(release_block(plan, plan->ws, plan->ws_device, dev));
-    plan->ws = nullptr;
-    plan->ws_bytes = 0;
-  }
-  if (!plan->ws) {
-    size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
-    s = cuda_status(cudaMalloc(&plan->ws, want), "cudaMalloc(workspace)");
-    if (s != TP_OK) {
-      plan->ws = nullptr;
-      return s;
+    if (b.device != cur) cudaSetDevice(cur);
+    if (freed) {
+      b = Block{};
+      return TP_OK;
     }
-    plan->ws_bytes = want;
-    plan->ws_device = dev;
   }
-  *out = plan->ws;
+  Retired* r = new (std::nothrow) Retired{b, plan->retired};
+  if (!r) return fail(TP_ERR_ARG, "out of host memory for the plan's workspace");
+  plan->retired = r;
+  b = Block{};
   return TP_OK;
 }
 
-tp_status plan_counters(tp_plan* plan, cudaStream_t st, unsigned** out) {
+// b as a block of at least `bytes` on the current device for work on st.
+static tp_status take_block(tp_plan* plan, Block& b, size_t bytes, cudaStream_t st, const char* what, void** out) {
   int dev = 0;
-  tp_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
-  if (s != TP_OK) return s;
-  if (plan->cnt && plan->cnt_device == dev) {
-    *out = plan->cnt;
-    return TP_OK;
+  TP_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  const bool in_capture = capturing(st);
+  if (!b.p || b.bytes < bytes || b.device != dev) {
+    TP_TRY(release_block(plan, b, dev, in_capture));
+    const size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
+    void* p = nullptr;
+    // an allocation is no part of a capture, and does not disturb it
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (in_capture) cudaThreadExchangeStreamCaptureMode(&mode);
+    const cudaError_t e = cudaMalloc(&p, want);
+    if (in_capture) cudaThreadExchangeStreamCaptureMode(&mode);
+    TP_TRY(cuda_status(e, what));
+    b.p = p;
+    b.bytes = want;
+    b.device = dev;
   }
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) {
-    cudaGetLastError();
-    return fail(TP_ERR_ARG, "the plan's first reduction on a device must run before a stream capture");
-  }
-  if (plan->cnt) {  // moved to another device
-    cudaDeviceSynchronize();
-    cudaSetDevice(plan->cnt_device);
-    cudaFree(plan->cnt);
-    cudaSetDevice(dev);
-    plan->cnt = nullptr;
-  }
-  void* p = nullptr;
-  s = cuda_status(cudaMalloc(&p, 2 * kPlanCounters * sizeof(unsigned)), "cudaMalloc(counters)");
-  if (s != TP_OK) return s;
-  // zero, and finished, before any kernel on any stream can use them
-  s = cuda_status(cudaMemsetAsync(p, 0, 2 * kPlanCounters * sizeof(unsigned), st), "cudaMemsetAsync(counters)");
-  if (s == TP_OK) s = cuda_status(cudaStreamSynchronize(st), "cudaStreamSynchronize(counters)");
-  if (s != TP_OK) {
-    cudaFree(p);
-    return s;
-  }
-  plan->cnt = static_cast<unsigned*>(p);
-  plan->cnt_device = dev;
-  *out = plan->cnt;
+  if (in_capture) b.held = true;
+  *out = b.p;
   return TP_OK;
 }
 
-tp_status workspace2(tp_plan* plan, size_t bytes, void** out) {
-  int dev = 0;
-  tp_status s = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
-  if (s != TP_OK) return s;
-  if (plan->ws2 && (plan->ws2_bytes < bytes || plan->ws2_device != dev)) {
-    TP_TRY(release_block(plan, plan->ws2, plan->ws2_device, dev));  // side-stream work may still use it
-    plan->ws2 = nullptr;
-    plan->ws2_bytes = 0;
-  }
-  if (!plan->ws2) {
-    size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
-    s = cuda_status(cudaMalloc(&plan->ws2, want), "cudaMalloc(side workspace)");
-    if (s != TP_OK) {
-      plan->ws2 = nullptr;
-      return s;
-    }
-    plan->ws2_bytes = want;
-    plan->ws2_device = dev;
-  }
-  *out = plan->ws2;
-  return TP_OK;
+tp_status workspace(tp_plan* plan, size_t bytes, cudaStream_t st, void** out) {
+  return take_block(plan, plan->ws, bytes, st, "cudaMalloc(workspace)", out);
+}
+
+tp_status workspace2(tp_plan* plan, size_t bytes, cudaStream_t st, void** out) {
+  return take_block(plan, plan->ws2, bytes, st, "cudaMalloc(side workspace)", out);
 }
 
 tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out) {
   int dev = 0;
   TP_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  const Block& b = plan->sc;
+  if ((!b.p || b.bytes < bytes || b.device != dev) && capturing(st))
+    return fail(TP_ERR_ARG, "the plan's workspace must grow to %zu bytes: make the call once before the stream capture", bytes);
+  return take_block(plan, plan->sc, bytes, st, "cudaMalloc(scratch)", out);
+}
+
+tp_status plan_counters(tp_plan* plan, cudaStream_t st, unsigned** out) {
+  int dev = 0;
+  TP_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  Block& b = plan->cnt;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  TP_TRY(cuda_status(cudaStreamIsCapturing(st, &cs), "cudaStreamIsCapturing"));
-  const bool capturing = cs != cudaStreamCaptureStatusNone;
-  if (!plan->sc || plan->sc_bytes < bytes || plan->sc_device != dev) {
-    if (capturing)
-      return fail(TP_ERR_ARG, "the plan's workspace must grow to %zu bytes: make the call once before the stream capture",
-                  bytes);
-    if (plan->sc) TP_TRY(release_block(plan, plan->sc, plan->sc_device, dev));
-    plan->sc = nullptr;
-    plan->sc_bytes = 0;
-    const size_t want = bytes < (1u << 20) ? (1u << 20) : bytes;
+  const bool in_capture = cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone;
+  cudaGetLastError();
+  if (!b.p || b.device != dev) {
+    if (in_capture) return fail(TP_ERR_ARG, "the plan's first reduction on a device must run before a stream capture");
+    TP_TRY(release_block(plan, b, dev, false));  // moved to another device
+    constexpr size_t bytes = 2 * kPlanCounters * sizeof(unsigned);
     void* p = nullptr;
-    TP_TRY(cuda_status(cudaMalloc(&p, want), "cudaMalloc(scratch)"));
-    plan->sc = p;
-    plan->sc_bytes = want;
-    plan->sc_device = dev;
+    TP_TRY(cuda_status(cudaMalloc(&p, bytes), "cudaMalloc(counters)"));
+    // zero, and finished, before any kernel on any stream can use them
+    tp_status s = cuda_status(cudaMemsetAsync(p, 0, bytes, st), "cudaMemsetAsync(counters)");
+    if (s == TP_OK) s = cuda_status(cudaStreamSynchronize(st), "cudaStreamSynchronize(counters)");
+    if (s != TP_OK) {
+      cudaFree(p);
+      return s;
+    }
+    b.p = p;
+    b.bytes = bytes;
+    b.device = dev;
   }
-  if (capturing) plan->captured = 1;
-  *out = plan->sc;
+  if (in_capture) b.held = true;
+  *out = static_cast<unsigned*>(b.p);
   return TP_OK;
 }
 
@@ -498,7 +462,7 @@ tp_status run_wgrad(tp_plan* plan, GemmBatch w, cudaStream_t st, bool allow_spli
   const int s = wgrad_split(plan, w, allow_split);
   if (s <= 1) return launch_gemm_bf16(w, st);
   void* ws = nullptr;
-  TP_TRY(workspace(plan, static_cast<size_t>(s) * w.n * w.g[0].M * w.g[0].N * sizeof(float), &ws));
+  TP_TRY(workspace(plan, static_cast<size_t>(s) * w.n * w.g[0].M * w.g[0].N * sizeof(float), st, &ws));
   return launch_gemm_split(w, s, static_cast<float*>(ws), st);
 }
 
@@ -611,18 +575,11 @@ tp_status tp_plan_create(int hidden, int ffn, int heads, int p, tp_dtype dtype, 
   plan->dtype = dtype;
   plan->partial_dtype = partial_dtype;
   plan->act = act;
-  plan->ws = nullptr;
-  plan->ws_bytes = 0;
-  plan->ws_device = -1;
-  plan->cnt = nullptr;
-  plan->cnt_device = -1;
   plan->defer_bwd = 0;
-  plan->ws2 = nullptr;
-  plan->ws2_bytes = 0;
-  plan->ws2_device = -1;
   plan->group_wgrad = 0;
   plan->wg_pend = nullptr;
   plan->wg_st = nullptr;
+  plan->retired = nullptr;
   *out = plan;
   return TP_OK;
 }
@@ -633,32 +590,17 @@ void tp_plan_destroy(tp_plan* plan) {
   plan->wg_pend = nullptr;
   int cur = 0;
   cudaGetDevice(&cur);
-  if (plan->ws) {
-    cudaSetDevice(plan->ws_device);
+  auto release = [](const tpi::Block& b) {
+    if (!b.p) return;
+    cudaSetDevice(b.device);
     cudaDeviceSynchronize();
-    cudaFree(plan->ws);
-  }
-  if (plan->cnt) {
-    cudaSetDevice(plan->cnt_device);
-    cudaDeviceSynchronize();
-    cudaFree(plan->cnt);
-  }
-  if (plan->ws2) {
-    cudaSetDevice(plan->ws2_device);
-    cudaDeviceSynchronize();
-    cudaFree(plan->ws2);
-  }
-  if (plan->sc) {
-    cudaSetDevice(plan->sc_device);
-    cudaDeviceSynchronize();
-    cudaFree(plan->sc);
-  }
+    cudaFree(b.p);
+  };
+  for (const tpi::Block* b : {&plan->ws, &plan->cnt, &plan->ws2, &plan->sc}) release(*b);
   while (plan->retired) {
     tpi::Retired* r = plan->retired;
     plan->retired = r->next;
-    cudaSetDevice(r->device);
-    cudaDeviceSynchronize();
-    cudaFree(r->p);
+    release(r->b);
     delete r;
   }
   cudaSetDevice(cur);
@@ -1238,7 +1180,6 @@ tp_status tp_layernorm_bwd(tp_plan* plan, int64_t rows, const void* x, const voi
   TP_TRY(check_ptr(dbeta, "dbeta"));
   if (dres) TP_TRY(check_ptr(dres, "dres"));
   TP_TRY(check_ln(plan));
-  note_capture(plan, as_stream(stream));
   return launch_layernorm_bwd(plan, x, gamma, dy, mean, rstd, dres, dx, dgamma, dbeta, accumulate,
                               rows, plan->hidden, plan->dtype, as_stream(stream));
 }
@@ -1286,8 +1227,7 @@ tp_status tp_embedding_bwd(tp_plan* plan, int64_t T, const int32_t* ids, const v
   size_t bytes = 0;
   TP_TRY(embedding_bwd_workspace(T, plan->vocab_padded, &bytes));
   void* ws = nullptr;
-  note_capture(plan, as_stream(stream));
-  TP_TRY(workspace(plan, bytes, &ws));
+  TP_TRY(workspace(plan, bytes, as_stream(stream), &ws));
   return launch_embedding_bwd(ids, T, dY, plan->hidden, plan->vocab, plan->vocab_padded,
                               plan->vocab_padded / p, to_marr(dE, p), plan->dtype, ws,
                               as_stream(stream));
@@ -1395,7 +1335,6 @@ tp_status tp_norm_sharded_bwd(tp_plan* plan, tp_norm_kind kind, int64_t rows, co
     dg.p[i] = dgamma[i];
     db.p[i] = dbeta ? dbeta[i] : nullptr;
   }
-  note_capture(plan, as_stream(stream));
   return launch_norm_sharded_bwd(plan, kind == TP_NORM_RMS, to_arr(X, p), to_arr(gamma, p),
                                  to_arr(dY, p), to_marr(dX, p), dg, db, p, rows, plan->hidden, mean,
                                  rstd, plan->dtype, as_stream(stream));
@@ -1532,7 +1471,6 @@ tp_status tp_column_sum(tp_plan* plan, int64_t rows, int64_t cols, const void* x
   if (rows > 0) TP_TRY(check_ptr(x, "x"));
   TP_TRY(check_ptr(out, "out"));
   TP_TRY(check_row_bytes(cols, plan->dtype, "cols"));
-  note_capture(plan, as_stream(stream));
   return launch_column_sum(plan, x, rows, cols, cols, out, accumulate, plan->dtype,
                            as_stream(stream));
 }
@@ -1568,7 +1506,6 @@ tp_status tp_attention_bwd(tp_plan* plan, int batch, int seq, const void* const*
   TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dQKV), p, "dQKV", false));
   if (plan->head_dim != 64 && plan->head_dim != 128)
     return fail(TP_ERR_UNSUPPORTED, "attention supports head_dim 64 or 128 (got %d)", plan->head_dim);
-  note_capture(plan, as_stream(stream));
   return launch_attention_bwd(plan, batch, seq, to_arr(QKV, p), to_arr(O, p), to_arr(dO, p), LSE,
                               to_marr(dQKV, p), as_stream(stream));
 }
@@ -1596,7 +1533,6 @@ tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void* dY,
   TP_TRY(check_row_bytes(h, plan->dtype, "hidden"));
   if (T == 0) return TP_OK;
   cudaStream_t st = as_stream(stream);
-  note_capture(plan, st);
 
   // dH_i = dY W_i (W_i is [h, k]: (n = j, k = c) at W_i + c*k + j -> MN-major B),
   // with the activation derivative fused in the epilogue.
@@ -1704,7 +1640,6 @@ static tp_status column_bwd_common(tp_plan* plan, tp_which which, int64_t T, con
   TP_TRY(check_row_bytes(h, plan->dtype, "hidden"));
   if (mode == 0) TP_TRY(check_row_bytes(h, plan->partial_dtype, "hidden (dX partials)"));
   if (T == 0) return TP_OK;
-  note_capture(plan, st);
   GemmBatch w{};
   if (dW) {
     // dW_i [n, h] = dZ_i^T X: A(m, t) = dZ_i[t, m] (MN-major), B(c, t) = X[t, c] (MN-major).
@@ -1874,7 +1809,6 @@ tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void*
   TP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dZ), p, "dZ", false));
   for (int i = 0; H && i < p; ++i)
     if (H[i] == dZ[i]) return fail(TP_ERR_ARG, "H[%d] must not alias dZ[%d]", i, i);
-  note_capture(plan, st);
   GemmBatch b{};
   b.n = p;
   b.b_mn = true;

@@ -846,7 +846,7 @@ tp_status launch_attention_bwd(tp_plan* plan, int batch, int seq, const PtrArray
   const char* e_ds = getenv("TP_ATTN_BWD_DS");
   const bool store_ds = !(e_ds && e_ds[0] == '0') && ds_bytes <= kDsBytesMax;
   void* ws = nullptr;
-  tp_status s = workspace(plan, vec_bytes + (store_ds ? ds_bytes : 0), &ws);
+  tp_status s = workspace(plan, vec_bytes + (store_ds ? ds_bytes : 0), st, &ws);
   if (s != TP_OK) return s;
   static BwdParams prm;
   static std::mutex mu;

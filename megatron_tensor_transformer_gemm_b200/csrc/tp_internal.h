@@ -10,10 +10,17 @@
 
 namespace tpi {
 struct GemmBatch;
-// A scratch block kept for the captured graphs that use it.
+// Device memory of a plan. held: it was handed to a call in a stream capture, so a graph
+// may replay with its address; when a larger block replaces it, it is kept until the plan
+// is destroyed.
+struct Block {
+  void* p = nullptr;
+  size_t bytes = 0;
+  int device = -1;
+  bool held = false;
+};
 struct Retired {
-  void* p;
-  int device;
+  Block b;
   Retired* next;
 };
 }
@@ -30,20 +37,15 @@ struct tp_plan {
   tp_dtype partial_dtype;  // element type of the full-shape partial sums
   tp_act act;
   // Device scratch, allocated on first need (cudaMalloc), grown on demand.
-  void* ws;
-  size_t ws_bytes;
-  int ws_device;
+  tpi::Block ws;
   // Arrival counters of single-launch reductions (zero at rest: the last
   // block of each reduction sets its counter back), allocated on first need;
   // the upper half serves work deferred to the side stream.
-  unsigned* cnt;
-  int cnt_device;
+  tpi::Block cnt;
   // Deferred backward (tp_set_backward_defer): weight gradients and bias sums
   // run on the device's side stream, with scratch of their own (ws2).
   int defer_bwd;
-  void* ws2;
-  size_t ws2_bytes;
-  int ws2_device;
+  tpi::Block ws2;
   // Grouped weight gradients (tp_set_wgrad_grouping): the row backward's
   // weight-gradient batch waits here (launched by the next column backward
   // together with its own, or by tp_flush_wgrad) on stream wg_st.
@@ -51,14 +53,8 @@ struct tp_plan {
   tpi::GemmBatch* wg_pend;  // NULL when nothing waits
   cudaStream_t wg_st;
   // Scratch of the calls that refuse to grow it inside a capture (tpi::scratch).
-  void* sc;
-  size_t sc_bytes;
-  int sc_device;
-  // Whether a call of this plan was captured into a graph: workspace blocks
-  // replaced since then are kept until the plan is destroyed, since the graph
-  // replays with their addresses.
-  int captured;
-  tpi::Retired* retired;
+  tpi::Block sc;
+  tpi::Retired* retired;  // replaced blocks that a graph may hold
 };
 
 namespace tpi {
@@ -113,11 +109,8 @@ tp_status persistent_grid(const void* kernel, int threads, int smem, int64_t uni
 
 // Device address of this device's status word (set by kernels on a timeout).
 tp_status device_status_word(unsigned** out);
-// Sets plan->captured when st is being captured (entry points that use the
-// plan's workspaces call it first).
-void note_capture(tp_plan* plan, cudaStream_t st);
-// Scratch of at least `bytes` on the current device, owned by the plan.
-tp_status workspace(tp_plan* plan, size_t bytes, void** out);
+// Scratch of at least `bytes` on the current device for work on `st`, owned by the plan.
+tp_status workspace(tp_plan* plan, size_t bytes, cudaStream_t st, void** out);
 // The plan's kPlanCounters arrival counters on the current device (zero at
 // rest). The first call on a device allocates and zeroes them (not allowed
 // while `st` is being captured).
@@ -125,12 +118,12 @@ constexpr int kPlanCounters = 4096;
 tp_status plan_counters(tp_plan* plan, cudaStream_t st, unsigned** out);
 // Scratch for the work a deferred backward puts on the side stream (never
 // shared with the caller's stream).
-tp_status workspace2(tp_plan* plan, size_t bytes, void** out);
+tp_status workspace2(tp_plan* plan, size_t bytes, cudaStream_t st, void** out);
 
 // Scratch of at least `bytes` on the current device for a call on `st`, owned
 // by the plan and shared by its calls in turn. Growing it allocates, so inside
 // a stream capture a call that needs more than the plan holds is refused
-// (TP_ERR_ARG), and it sets plan->captured as note_capture does.
+// (TP_ERR_ARG).
 tp_status scratch(tp_plan* plan, size_t bytes, cudaStream_t st, void** out);
 
 // Validation helpers: each returns TP_OK or records an error.

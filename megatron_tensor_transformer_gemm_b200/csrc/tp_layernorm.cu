@@ -415,7 +415,7 @@ tp_status launch_layernorm_bwd(tp_plan* plan, const void* x, const void* gamma, 
   const int64_t rps = rows > 0 ? (rows + splits - 1) / splits : 1;
   splits = rows > 0 ? (rows + rps - 1) / rps : 0;
   void* ws = nullptr;
-  tp_status s = workspace(plan, static_cast<size_t>(std::max<int64_t>(splits, 1)) * 2 * cols * sizeof(float), &ws);
+  tp_status s = workspace(plan, static_cast<size_t>(std::max<int64_t>(splits, 1)) * 2 * cols * sizeof(float), st, &ws);
   if (s != TP_OK) return s;
   float* part = static_cast<float*>(ws);
   if (rows > 0) {
@@ -922,7 +922,7 @@ tp_status launch_norm_sharded_bwd(tp_plan* plan, bool rms, const PtrArray& X, co
   if (s != TP_OK) return s;
   const int groups = grid > 2 * kParamGroup ? static_cast<int>((grid + kParamGroup - 1) / kParamGroup) : 0;
   void* ws = nullptr;
-  s = workspace(plan, static_cast<size_t>(grid + groups) * 2 * h * sizeof(float), &ws);
+  s = workspace(plan, static_cast<size_t>(grid + groups) * 2 * h * sizeof(float), st, &ws);
   if (s != TP_OK) return s;
   float* part = static_cast<float*>(ws);
   float* inter = part + grid * 2 * h;

@@ -494,7 +494,7 @@ tp_status launch_column_sum(tp_plan* plan, const void* x, int64_t rows, int64_t 
   const int64_t rps = rows > 0 ? (rows + splits - 1) / splits : 1;
   splits = rows > 0 ? (rows + rps - 1) / rps : 1;
   void* ws = nullptr;
-  tp_status s = workspace(plan, ws_offset + static_cast<size_t>(splits) * cols * sizeof(float), &ws);
+  tp_status s = workspace(plan, ws_offset + static_cast<size_t>(splits) * cols * sizeof(float), st, &ws);
   if (s != TP_OK) return s;
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ws_offset);
   if (rows > 0) {
@@ -531,7 +531,7 @@ static tp_status column_sum_grouped_impl(tp_plan* plan, const PtrArray& x, int n
   splits = rows > 0 ? (rows + rps - 1) / rps : 0;
   const size_t bytes = ws_offset + static_cast<size_t>(std::max<int64_t>(splits, 1)) * cols * n * sizeof(float);
   void* ws = nullptr;
-  tp_status s = deferred ? workspace2(plan, bytes, &ws) : workspace(plan, bytes, &ws);
+  tp_status s = deferred ? workspace2(plan, bytes, st, &ws) : workspace(plan, bytes, st, &ws);
   if (s != TP_OK) return s;
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ws_offset);
   if (rows > 0 && static_cast<int64_t>(gx) * n <= kPlanCounters) {
