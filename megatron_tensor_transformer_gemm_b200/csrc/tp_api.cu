@@ -1795,8 +1795,8 @@ tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void*
   if (dbias) TP_TRY(check_ptr(dbias, "dbias"));
   if (dW && !H) return fail(TP_ERR_ARG, "dW needs H, which it is the product with");
   cudaStream_t st = as_stream(stream);
-  TP_TRY(flush_wgrad(plan));
   if (T == 0) {  // sums over no token
+    TP_TRY(flush_wgrad(plan));
     for (int i = 0; dW && i < p; ++i)
       TP_TRY(cuda_status(cudaMemsetAsync(dW[i], 0, static_cast<size_t>(h) * k * 2, st), "cudaMemsetAsync(dW)"));
     if (dbias) TP_TRY(cuda_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(h) * 4, st), "cudaMemsetAsync(dbias)"));
@@ -1848,15 +1848,22 @@ tp_status tp_row_bwd_ckpt8(tp_plan* plan, int64_t T, const void* dY, const void*
       o.ldd = k;
     }
   }
-  // the workspace first: a call that a capture refuses has launched nothing
+  // the workspace first, the bias sum's partials and counters too: a call that a capture
+  // refuses has launched nothing
   const int s = dW ? gemm_split_k(w) : 1;
+  const size_t split_bytes = s > 1 ? (static_cast<size_t>(s) * p * h * k * sizeof(float) + 255) / 256 * 256 : 0;
+  const size_t sum_bytes = dbias ? column_sum_bytes(T, h, plan->dtype) : 0;
   void* part = nullptr;
-  if (s > 1) TP_TRY(scratch(plan, static_cast<size_t>(s) * p * h * k * sizeof(float), st, &part));
+  if (split_bytes + sum_bytes) TP_TRY(scratch(plan, split_bytes + sum_bytes, st, &part));
+  float* sum_part = reinterpret_cast<float*>(static_cast<uint8_t*>(part) + split_bytes);
+  unsigned* counters = nullptr;
+  if (dbias) TP_TRY(plan_counters(plan, st, &counters));
+  TP_TRY(flush_wgrad(plan));
   // dbias, a sum over dY alone, beside the products (40 -> 37 us at 2011 x 512 x 2048)
   const SideFork side(st, dbias && side_free(plan));
   TP_TRY(side.status());
   TP_TRY(launch_gemm_bf16(b, st));
-  if (dbias) TP_TRY(launch_column_sum(plan, dY, T, h, h, dbias, 0, plan->dtype, side.stream()));
+  if (dbias) TP_TRY(launch_column_sum_in(plan, dY, T, h, dbias, plan->dtype, sum_part, side.stream()));
   if (!dW) return TP_OK;
   return s > 1 ? launch_gemm_split(w, s, static_cast<float*>(part), st) : launch_gemm_bf16(w, st);
 }

@@ -165,6 +165,12 @@ tp_status launch_column_sum_deferred(tp_plan* plan, const PtrArray& x, int n, in
                                      int64_t cols, int64_t ld, const MutPtrArray& out, tp_dtype dt,
                                      cudaStream_t st);
 
+// One input's column sums with the partials in `part` (column_sum_bytes of them), for calls
+// that take their scratch before they launch anything.
+size_t column_sum_bytes(int64_t rows, int64_t cols, tp_dtype dt);
+tp_status launch_column_sum_in(tp_plan* plan, const void* x, int64_t rows, int64_t cols, float* out, tp_dtype dt,
+                               float* part, cudaStream_t st);
+
 // LayerNorm (tp_layernorm.cu).
 tp_status launch_layernorm_fwd(const PtrArray& x_seq, int n, int64_t rows_per_src, int64_t cols,
                                const void* gamma, const void* beta, void* y, float* mean,

@@ -515,25 +515,45 @@ tp_status launch_column_sum(tp_plan* plan, const void* x, int64_t rows, int64_t 
   return after_launch("column_sum/pass2");
 }
 
-// The grouped column sums with their scratch chosen by the caller: `deferred`
-// takes the side workspace and the upper half of the plan's counters.
-static tp_status column_sum_grouped_impl(tp_plan* plan, const PtrArray& x, int n, int64_t rows, int64_t cols,
-                                         int64_t ld, const MutPtrArray& out, int accumulate, tp_dtype dt,
-                                         cudaStream_t st, size_t ws_offset, bool deferred) {
-  if (n < 1 || n > TP_MAX_SHARDS) return fail(TP_ERR_ARG, "column sums of %d inputs", n);
-  const int V = dt == TP_BF16 ? 8 : 4;
-  const int64_t vpr = cols / V;
-  const int gx = static_cast<int>((vpr + 31) / 32);
-  int64_t splits = std::max<int64_t>(1, (static_cast<int64_t>(sm_count()) * 8) / (gx * n));
+namespace {
+// The row splits of the column sums of n inputs.
+struct ColumnSplit {
+  int64_t vpr, rps, splits;
+  int gx;
+  size_t bytes;  // of the splits' partials
+};
+ColumnSplit column_split(int n, int64_t rows, int64_t cols, tp_dtype dt) {
+  ColumnSplit c{};
+  c.vpr = cols / (dt == TP_BF16 ? 8 : 4);
+  c.gx = static_cast<int>((c.vpr + 31) / 32);
+  int64_t splits = std::max<int64_t>(1, (static_cast<int64_t>(sm_count()) * 8) / (c.gx * n));
   splits = std::min<int64_t>(splits, std::max<int64_t>(1, (rows + 63) / 64));
   splits = std::min<int64_t>(splits, 1024);
-  const int64_t rps = rows > 0 ? (rows + splits - 1) / splits : 1;
-  splits = rows > 0 ? (rows + rps - 1) / rps : 0;
-  const size_t bytes = ws_offset + static_cast<size_t>(std::max<int64_t>(splits, 1)) * cols * n * sizeof(float);
-  void* ws = nullptr;
-  tp_status s = deferred ? workspace2(plan, bytes, st, &ws) : workspace(plan, bytes, st, &ws);
-  if (s != TP_OK) return s;
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ws_offset);
+  c.rps = rows > 0 ? (rows + splits - 1) / splits : 1;
+  c.splits = rows > 0 ? (rows + c.rps - 1) / c.rps : 0;
+  c.bytes = static_cast<size_t>(std::max<int64_t>(c.splits, 1)) * cols * n * sizeof(float);
+  return c;
+}
+}  // namespace
+
+size_t column_sum_bytes(int64_t rows, int64_t cols, tp_dtype dt) { return column_split(1, rows, cols, dt).bytes; }
+
+// The grouped column sums with their scratch chosen by the caller: `part`, or the plan's
+// workspace, or with `deferred` the side workspace and the upper half of the plan's counters.
+static tp_status column_sum_grouped_impl(tp_plan* plan, const PtrArray& x, int n, int64_t rows, int64_t cols,
+                                         int64_t ld, const MutPtrArray& out, int accumulate, tp_dtype dt,
+                                         cudaStream_t st, size_t ws_offset, bool deferred, float* part = nullptr) {
+  if (n < 1 || n > TP_MAX_SHARDS) return fail(TP_ERR_ARG, "column sums of %d inputs", n);
+  const ColumnSplit c = column_split(n, rows, cols, dt);
+  const int64_t vpr = c.vpr, rps = c.rps, splits = c.splits;
+  const int gx = c.gx;
+  tp_status s = TP_OK;
+  if (!part) {
+    void* ws = nullptr;
+    s = deferred ? workspace2(plan, ws_offset + c.bytes, st, &ws) : workspace(plan, ws_offset + c.bytes, st, &ws);
+    if (s != TP_OK) return s;
+    part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ws_offset);
+  }
   if (rows > 0 && static_cast<int64_t>(gx) * n <= kPlanCounters) {
     // one launch: the last block of each column slab finishes it
     unsigned* ctr = nullptr;
@@ -566,6 +586,15 @@ tp_status launch_column_sum_grouped(tp_plan* plan, const PtrArray& x, int n, int
                                     int64_t cols, int64_t ld, const MutPtrArray& out, int accumulate,
                                     tp_dtype dt, cudaStream_t st, size_t ws_offset) {
   return column_sum_grouped_impl(plan, x, n, rows, cols, ld, out, accumulate, dt, st, ws_offset, false);
+}
+
+tp_status launch_column_sum_in(tp_plan* plan, const void* x, int64_t rows, int64_t cols, float* out, tp_dtype dt,
+                               float* part, cudaStream_t st) {
+  PtrArray X{};
+  MutPtrArray O{};
+  X.p[0] = x;
+  O.p[0] = out;
+  return column_sum_grouped_impl(plan, X, 1, rows, cols, cols, O, 0, dt, st, 0, false, part);
 }
 
 tp_status launch_column_sum_deferred(tp_plan* plan, const PtrArray& x, int n, int64_t rows,
