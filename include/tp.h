@@ -397,7 +397,9 @@ TP_API tp_status tp_attention_fwd(tp_plan* plan, int batch, int seq, const void*
  * on a side stream the library creates per device, forked from `stream` by an
  * event, and `stream` waits for it before the call returns: the results are
  * ordered on `stream` as with one stream, also inside a stream capture (the
- * fork and join become graph edges). Environment TP_BWD_CONCURRENT=0 keeps
+ * fork and join become graph edges). The eager calls of all host threads share
+ * one side stream; a capture has one of its own while it lasts, so calls of
+ * other threads, eager or in captures of theirs, may run meanwhile. Environment TP_BWD_CONCURRENT=0 keeps
  * every launch on `stream`. Calls on one plan must not overlap in time (they
  * share the plan's workspace). */
 
@@ -415,7 +417,8 @@ TP_API tp_status tp_set_backward_defer(tp_plan* plan, int on);
 
 /* Make `stream` wait for all work issued so far on the current device's side
  * stream (the deferred weight gradients and bias sums of every plan). An
- * event wait: it returns at once on the host, and works inside a capture. */
+ * event wait: it returns at once on the host. In a stream capture it joins the
+ * work deferred in that capture (TP_ERR_ARG if there is none). */
 TP_API tp_status tp_backward_join(void* stream);
 
 /* Grouped weight gradients (on != 0): tp_row_bwd leaves its weight-gradient

@@ -132,7 +132,7 @@ tp_status device_status_word(unsigned** out) {
   return TP_OK;
 }
 
-static bool capturing(cudaStream_t st) {
+bool capturing(cudaStream_t st) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(st, &cs) == cudaSuccess) return cs != cudaStreamCaptureStatusNone;
   cudaGetLastError();
@@ -335,47 +335,93 @@ MutPtrArray to_marr(void* const* a, int n) {
 // side GEMM uses no workspace (the weight gradient's split-K partials and the
 // bias sums do, on the caller's stream). Works inside stream capture (the
 // fork and join become graph edges). TP_BWD_CONCURRENT=0 keeps one stream.
+//
+// Waiting for a captured stream draws the waiting one into its capture, so a capture
+// never uses the stream of the eager calls, nor that of another capture, which may go on
+// in other threads at the same time: each has a side stream of its own for as long as it
+// lasts (its calls share it, since deferred work is joined by a later one), which then
+// serves the next capture.
 struct SideStream {
   cudaStream_t s = nullptr;
   cudaEvent_t fork = nullptr, join = nullptr;
+  SideStream* next = nullptr;
 };
 
-tp_status side_stream(SideStream** out) {
-  constexpr int kMaxDev = 64;
-  static SideStream side[kMaxDev];
-  static std::mutex mu;
+std::mutex g_side_mu;
+SideStream* g_side[kMaxDevices] = {};  // per device, the eager calls' first
+
+tp_status new_side_stream(SideStream** out) {
+  SideStream* n = new (std::nothrow) SideStream;
+  if (!n) return fail(TP_ERR_ARG, "out of host memory for a side stream");
+  // creating a stream is no part of a capture
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  tp_status r = cuda_status(cudaStreamCreateWithFlags(&n->s, cudaStreamNonBlocking), "cudaStreamCreate(side)");
+  if (r == TP_OK) r = cuda_status(cudaEventCreateWithFlags(&n->fork, cudaEventDisableTiming), "cudaEventCreate(fork)");
+  if (r == TP_OK) r = cuda_status(cudaEventCreateWithFlags(&n->join, cudaEventDisableTiming), "cudaEventCreate(join)");
+  if (r != TP_OK) {
+    if (n->fork) cudaEventDestroy(n->fork);
+    if (n->s) cudaStreamDestroy(n->s);
+    delete n;
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (r == TP_OK) *out = n;
+  return r;
+}
+
+// The current device's side stream for work forked from st (g_side_mu is held): the eager
+// one, or that of st's capture. `make` = false: NULL where there is none yet.
+tp_status find_side_stream(cudaStream_t st, bool make, SideStream** out) {
+  *out = nullptr;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) {
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
     return fail(TP_ERR_NO_DEVICE, "no current CUDA device");
   }
-  std::lock_guard<std::mutex> lk(mu);
-  SideStream& sd = side[dev];
-  if (!sd.s) {
-    SideStream n;
-    tp_status r = cuda_status(cudaStreamCreateWithFlags(&n.s, cudaStreamNonBlocking), "cudaStreamCreate(side)");
-    if (r == TP_OK) r = cuda_status(cudaEventCreateWithFlags(&n.fork, cudaEventDisableTiming), "cudaEventCreate(fork)");
-    if (r == TP_OK) r = cuda_status(cudaEventCreateWithFlags(&n.join, cudaEventDisableTiming), "cudaEventCreate(join)");
-    if (r != TP_OK) {
-      if (n.join) cudaEventDestroy(n.join);
-      if (n.fork) cudaEventDestroy(n.fork);
-      if (n.s) cudaStreamDestroy(n.s);
-      return r;
-    }
-    sd = n;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  TP_TRY(cuda_status(cudaStreamGetCaptureInfo(st, &cs, &id), "cudaStreamGetCaptureInfo"));
+  if (cs == cudaStreamCaptureStatusInvalidated)
+    return fail(TP_ERR_CUDA, "the stream's capture was invalidated");
+  if (!g_side[dev] && make) TP_TRY(new_side_stream(&g_side[dev]));
+  if (!g_side[dev]) return TP_OK;
+  if (cs == cudaStreamCaptureStatusNone) {
+    *out = g_side[dev];
+    return TP_OK;
   }
-  *out = &sd;
+  SideStream* idle = nullptr;
+  for (SideStream* n = g_side[dev]->next; n; n = n->next) {
+    cudaStreamCaptureStatus ns = cudaStreamCaptureStatusNone;
+    unsigned long long nid = 0;
+    if (cudaStreamGetCaptureInfo(n->s, &ns, &nid) != cudaSuccess) {
+      cudaGetLastError();
+      continue;
+    }
+    if (ns != cudaStreamCaptureStatusNone && nid == id) {
+      *out = n;
+      return TP_OK;
+    }
+    if (ns == cudaStreamCaptureStatusNone) idle = n;
+  }
+  if (!make) return TP_OK;
+  if (!idle) {
+    TP_TRY(new_side_stream(&idle));
+    idle->next = g_side[dev]->next;
+    g_side[dev]->next = idle;
+  }
+  *out = idle;
   return TP_OK;
 }
 
-// The side stream waits for st. One event serves every call on the device, so the
-// record and the wait on it are one step for the host's threads: between them another
-// thread's record would make the side stream wait for that thread's stream instead.
-tp_status side_wait(SideStream* sd, cudaStream_t st) {
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lk(mu);
-  TP_TRY(cuda_status(cudaEventRecord(sd->fork, st), "cudaEventRecord(fork)"));
-  return cuda_status(cudaStreamWaitEvent(sd->s, sd->fork, 0), "cudaStreamWaitEvent(fork)");
+// Fork: the side stream for st's work waits for st. Choosing it, recording the event and
+// waiting on it are one step for the host's threads: between them another thread's record
+// would make the side stream wait for that thread's stream instead, or its capture take
+// the stream.
+tp_status side_fork(cudaStream_t st, SideStream** out) {
+  std::lock_guard<std::mutex> lk(g_side_mu);
+  TP_TRY(find_side_stream(st, true, out));
+  TP_TRY(cuda_status(cudaEventRecord((*out)->fork, st), "cudaEventRecord(fork)"));
+  return cuda_status(cudaStreamWaitEvent((*out)->s, (*out)->fork, 0), "cudaStreamWaitEvent(fork)");
 }
 
 bool side_stream_on() {
@@ -390,8 +436,7 @@ namespace tpi {
 SideFork::SideFork(cudaStream_t st, bool on) : st_(st), s_(st) {
   if (!on) return;
   SideStream* sd = nullptr;
-  status_ = side_stream(&sd);
-  if (status_ == TP_OK) status_ = side_wait(sd, st);
+  status_ = side_fork(st, &sd);
   if (status_ != TP_OK) return;
   s_ = sd->s;
   join_ = sd->join;
@@ -627,9 +672,14 @@ tp_status tp_set_wgrad_grouping(tp_plan* plan, int on) {
 }
 
 tp_status tp_backward_join(void* stream) {
-  SideStream* sd = nullptr;
-  TP_TRY(side_stream(&sd));
   cudaStream_t st = as_stream(stream);
+  SideStream* sd = nullptr;
+  std::lock_guard<std::mutex> lk(g_side_mu);
+  TP_TRY(find_side_stream(st, false, &sd));
+  if (!sd) {
+    if (capturing(st)) return fail(TP_ERR_ARG, "nothing was deferred in this stream capture: there is no work to join");
+    return TP_OK;  // no call has used the side stream yet
+  }
   TP_TRY(cuda_status(cudaEventRecord(sd->join, sd->s), "cudaEventRecord(join)"));
   return cuda_status(cudaStreamWaitEvent(st, sd->join, 0), "cudaStreamWaitEvent(join)");
 }
@@ -1583,8 +1633,7 @@ tp_status tp_row_bwd(tp_plan* plan, tp_which which, int64_t T, const void* dY,
     // joined by tp_backward_join (dW without a K split: no shared scratch).
     TP_TRY(flush_wgrad(plan));
     SideStream* sd = nullptr;
-    TP_TRY(side_stream(&sd));
-    TP_TRY(side_wait(sd, st));
+    TP_TRY(side_fork(st, &sd));
     TP_TRY(run_gemm(plan, b, st));
     if (dW) TP_TRY(launch_gemm_bf16(w, sd->s));
     if (dbias) {
@@ -1696,8 +1745,7 @@ static tp_status column_bwd_common(tp_plan* plan, tp_which which, int64_t T, con
     // joined by tp_backward_join (dW without a K split: no shared scratch).
     TP_TRY(flush_wgrad(plan));
     SideStream* sd = nullptr;
-    TP_TRY(side_stream(&sd));
-    TP_TRY(side_wait(sd, st));
+    TP_TRY(side_fork(st, &sd));
     if (has_dx) TP_TRY(run_gemm(plan, d, st));
     if (dW) TP_TRY(launch_gemm_bf16(w, sd->s));
     if (dbias)
