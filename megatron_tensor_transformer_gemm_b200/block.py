@@ -51,10 +51,13 @@ class TPMLP:
         grouped launch (tp_set_wgrad_grouping; backward() issues both). Off by
         default: on the 7B step it measured slower than two launches.
         ckpt8: keep the pre-activation for the backward as 8-bit codes and scales
-        (tp_column_fwd_ckpt8) and compute the activation again there, so that
-        between the passes the MLP holds 1.03 bytes per pre-activation element in
-        place of the 2 of Z and the 2 of H. H is then scratch within a pass:
-        H_scratch (a list of p [T, ffn/p] tensors) lets layers share it."""
+        (tp_column_fwd_ckpt8) and compute the activation again there. Between the
+        passes the MLP then holds 1.03 bytes per pre-activation element in place of
+        the 2 of Z, the 2 of dZ and H's: H and dZ are taken for a pass only, from
+        the caching allocator (by a captured step from its graph's own pool), so
+        that layers that run one after the other use the same memory. A plan with
+        deferred weight gradients, which read dZ after the backward has returned,
+        keeps its dZ. H_scratch (a list of p [T, ffn/p] tensors): used for H."""
         if H_scratch is not None and not ckpt8:
             raise ValueError("H_scratch needs ckpt8: without it H is kept from the forward for the backward")
         self.ckpt8, self._H_scratch = ckpt8, H_scratch
@@ -99,17 +102,21 @@ class TPMLP:
             self.Zs = [_empty(scales, torch.uint8, dev) for _ in range(p)]
         else:
             self.Z = [_empty((T, self.n1), dt, dev) for _ in range(p)]
-        self.H = self._H_scratch or [_empty((T, self.fp), dt, dev) for _ in range(p)]
+            self.H = [_empty((T, self.fp), dt, dev) for _ in range(p)]
         self.P = None if self.fused else [_empty((T, self.h), dt, dev) for _ in range(p)]
         self.Y = _empty((T, self.h), dt, dev)
         if backward:
-            self.dZ = [_empty((T, self.n1), dt, dev) for _ in range(p)]
+            self.dZ = None if self.ckpt8 else [_empty((T, self.n1), dt, dev) for _ in range(p)]
             self.dXp = None if self.fused else [_empty((T, self.h), dt, dev) for _ in range(p)]
             self.dX = _empty((T, self.h), dt, dev)
             self.dW1 = [torch.empty_like(w) for w in self.W1]
             self.dW2 = [torch.empty_like(w) for w in self.W2]
             self.db1 = [_empty((self.n1,), torch.float32, dev) for _ in range(p)] if self.bias else None
             self.db2 = _empty((self.h,), torch.float32, dev) if self.bias else None
+
+    def _scratch(self, T: int, n: int) -> list:
+        """p shards of [T, n] for the calls of one pass, in one allocation (8-9 us on the host)."""
+        return list(_empty((self.p, T, n), self.dt, self.device).unbind(0))
 
     # ---------------------------------------------------------------- passes
     def forward(self, X: torch.Tensor, residual=None, out=None):
@@ -118,21 +125,23 @@ class TPMLP:
         self.X = X
         pl = self.plan
         if self.ckpt8:
-            pl.column_fwd_ckpt8(T, X, self.W1, self.b1, self.Zq, self.Zs, self.H)
+            H = self._H_scratch or self._scratch(T, self.fp)
+            pl.column_fwd_ckpt8(T, X, self.W1, self.b1, self.Zq, self.Zs, H)
         else:
-            pl.column_fwd("mlp", T, X, self.W1, self.b1, self.Z if self.act != "none" else None, self.H)
+            H = self.H
+            pl.column_fwd("mlp", T, X, self.W1, self.b1, self.Z if self.act != "none" else None, H)
         Y = self.Y if out is None else out
         if self.fused:
-            pl.row_fwd_reduce("mlp", T, self.H, self.W2, self.b2, residual, Y)
+            pl.row_fwd_reduce("mlp", T, H, self.W2, self.b2, residual, Y)
         elif self.chunks:
             self._overlapped(T, lambda r0, r1: pl.row_fwd_partial(
-                                 "mlp", r1 - r0, [h[r0:r1] for h in self.H], self.W2,
+                                 "mlp", r1 - r0, [h[r0:r1] for h in H], self.W2,
                                  [q[r0:r1] for q in self.P]),
                              lambda r0, r1: pl.reduce_partials(
                                  r1 - r0, [q[r0:r1] for q in self.P], self.b2,
                                  None if residual is None else residual[r0:r1], Y[r0:r1]))
         else:
-            pl.row_fwd_partial("mlp", T, self.H, self.W2, self.P)
+            pl.row_fwd_partial("mlp", T, H, self.W2, self.P)
             pl.reduce_partials(T, self.P, self.b2, residual, Y)
         return Y
 
@@ -167,25 +176,28 @@ class TPMLP:
         T = dY.shape[0]
         pl = self.plan
         if self.ckpt8:
-            pl.row_bwd_ckpt8(T, dY, self.W2, self.Zq, self.Zs, self.H, self.dZ, self.dW2, self.db2)
+            dZ = self.dZ or self._scratch(T, self.n1)
+            if pl.backward_deferred:
+                self.dZ = dZ
+            pl.row_bwd_ckpt8(T, dY, self.W2, self.Zq, self.Zs, self._H_scratch or self._scratch(T, self.fp), dZ, self.dW2, self.db2)
         else:
-            pl.row_bwd("mlp", T, dY, self.H, self.W2, self.Z if self.act != "none" else None, self.dZ,
-                       self.dW2, self.db2)
+            dZ = self.dZ
+            pl.row_bwd("mlp", T, dY, self.H, self.W2, self.Z if self.act != "none" else None, dZ, self.dW2, self.db2)
         dX = self.dX if out is None else out
         if self.fused:
-            pl.column_bwd_reduce("mlp", T, self.X, self.dZ, self.W1, self.dW1, self.db1, dX)
+            pl.column_bwd_reduce("mlp", T, self.X, dZ, self.W1, self.dW1, self.db1, dX)
         elif self.chunks:
             # dX block by block with the reduces overlapped; the weight gradient
             # last, so the final block's reduce runs under it too.
             self._overlapped(T, lambda r0, r1: pl.column_bwd(
-                                 "mlp", r1 - r0, None, [z[r0:r1] for z in self.dZ], self.W1, None,
+                                 "mlp", r1 - r0, None, [z[r0:r1] for z in dZ], self.W1, None,
                                  None, [q[r0:r1] for q in self.dXp]),
                              lambda r0, r1: pl.reduce_partials(
                                  r1 - r0, [q[r0:r1] for q in self.dXp], None, None, dX[r0:r1]),
-                             tail=lambda: pl.column_bwd("mlp", T, self.X, self.dZ, self.W1,
+                             tail=lambda: pl.column_bwd("mlp", T, self.X, dZ, self.W1,
                                                         self.dW1, self.db1, None))
         else:
-            pl.column_bwd("mlp", T, self.X, self.dZ, self.W1, self.dW1, self.db1, self.dXp)
+            pl.column_bwd("mlp", T, self.X, dZ, self.W1, self.dW1, self.db1, self.dXp)
             pl.reduce_partials(T, self.dXp, None, None, dX)
         return dX
 

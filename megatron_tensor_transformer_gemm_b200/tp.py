@@ -288,6 +288,8 @@ class Plan:
     """A tp_plan: block dimensions, shard count p, dtype, activation and the
     dtype of the full-shape partial sums (default: the plan dtype)."""
 
+    backward_deferred = False  # set_backward_defer
+
     def __init__(self, hidden: int, ffn: int, heads: int, p: int, dtype: str = "bf16",
                  act: str = "gelu", partial_dtype: str | None = None):
         self.hidden, self.ffn, self.heads, self.p = hidden, ffn, heads, p
@@ -575,6 +577,7 @@ class Plan:
         """tp_set_backward_defer: this plan's backward calls leave their weight
         gradients and bias sums on the side stream until backward_join()."""
         check(lib.tp_set_backward_defer(self._h, 1 if on else 0), "tp_set_backward_defer")
+        self.backward_deferred = bool(on)
 
     def column_sum(self, rows, cols, x, out, accumulate=False, stream=None):
         check(lib.tp_column_sum(self._h, rows, cols, _ptr(x), _ptr(out), 1 if accumulate else 0,
