@@ -33,7 +33,8 @@
  *   - Every device pointer must be 16-byte aligned and every row (the
  *     innermost extent times the element size) a multiple of 16 bytes.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream). Calls are
- *     asynchronous on it; they take no locks and never synchronise.
+ *     asynchronous on it: they hold locks only for host bookkeeping, and wait for
+ *     the device only to replace a plan's workspace by a larger one.
  *   - Ownership: the caller owns every tensor. The plan owns host metadata and
  *     a device workspace that the library allocates (cudaMalloc) the first
  *     time a call needs scratch space, replaces by a larger one when a call needs

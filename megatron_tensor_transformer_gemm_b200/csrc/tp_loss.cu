@@ -23,10 +23,11 @@
 // computed once: 6 T V h operations for loss and gradients, against
 // 8 for recomputing the scores in the backward, at 6 bytes of traffic per score.
 // fp32 plans keep the chunk's scores in fp32.
-// Bound by the tensor cores: 4096 x 131072 x 4096 over 8 shards in 10.6 ms, 1245
-// TFLOP/s at the power limit (scores 3.4, rows 0.4, dX 3.2, dW 3.5 ms); 2048 x 32000 x
-// 512 in 290 us replayed, 694 TFLOP/s: its tiles have 8 K blocks, shorter than the
-// epilogue; 61 tokens' losses in 55 us, W read once at 4.8 TB/s.
+// Bound by the tensor cores: 4096 x 131072 x 4096 over 8 shards in 10.6-11.4 ms, 1160-1247
+// TFLOP/s at the power limit of the GPU at hand (scores 3.4, rows 0.4, dX 3.2, dW 3.5 ms);
+// 32768 tokens of it, in 8 chunks, 91 ms, 1159; 2048 x 32000 x 512 in 290 us replayed, 694
+// TFLOP/s: its tiles have 8 K blocks, shorter than the epilogue; 61 tokens' losses in
+// 55 us, W read once at 4.8 TB/s.
 #include <algorithm>
 
 #include "tp_device.cuh"
